@@ -13,6 +13,7 @@
 
 #include "w4a16.h"
 #include "w4a16_internal.hpp"
+#include "w4a16_routed.hpp"
 
 using namespace w4a16;
 
@@ -40,7 +41,9 @@ constexpr int kMaxDevices = 64;
 // 0 = not checked yet, 1 = gfx950, 2 = another architecture
 std::atomic<int> g_arch_state[kMaxDevices];
 
-int32_t arch_gate() {
+}  // namespace
+
+int32_t w4a16::arch_gate() {
     int dev = -1;
     hipError_t e = hipGetDevice(&dev);
     if (e != hipSuccess) {
@@ -64,6 +67,8 @@ int32_t arch_gate() {
     }
     return state == 1 ? W4A16_OK : W4A16_ERR_ARCH;
 }
+
+namespace {
 
 std::mutex g_scratch_mu;
 std::atomic<void *> g_scratch_ptr[kMaxDevices];
@@ -99,15 +104,15 @@ int32_t scratch_of_current_device(void **out) {
     return W4A16_OK;
 }
 
-int32_t finish_launch(const char *what, int err) {
+}  // namespace
+
+int32_t w4a16::finish_launch(const char *what, int err) {
     if (err != (int)hipSuccess) {
         set_hip_error(what, (hipError_t)err);
         return W4A16_ERR_HIP;
     }
     return W4A16_OK;
 }
-
-}  // namespace
 
 extern "C" {
 

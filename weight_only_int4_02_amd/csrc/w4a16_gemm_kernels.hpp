@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "w4a16_kernels.hpp"
+#include "w4a16_lora.hpp"
 
 namespace w4a16 {
 
@@ -358,8 +359,10 @@ __device__ __forceinline__ void small_wait(int after) {
     }
 }
 
-template <int W, int NB, int MT, int JPG, int D, bool BF, bool XL = false>
-__global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a) {
+// EXT: what is added to the fp32 results before they are rounded (LoraExt), or
+// nothing (NoExt).
+template <int W, int NB, int MT, int JPG, int D, bool BF, bool XL = false, typename EXT = NoExt>
+__global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a, EXT ext) {
     static_assert(D >= 2 && D <= 12, "ring of 2..12 stages");
     using Stage = SmallStage<NB, MT, JPG, XL>;
     constexpr int LPS = Stage::LOADS;
@@ -479,6 +482,10 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a) {
         const int m0 = m_base + t * 16 + 4 * (l >> 4);
         if (n >= a.N)
             continue;
+        if constexpr (EXT::on) {
+            if (blockIdx.z == 0)
+                lora_add4<BF>(ext.l, a.M, a.N, m0, n, v);
+        }
         if (a.splits == 1) {
 #pragma unroll
             for (int rr = 0; rr < 4; rr++) {
@@ -509,9 +516,10 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a) {
 // will do: row r of the product only feeds output row r, which is never
 // stored).  Otherwise as gemm_small_m_kernel.
 // ---------------------------------------------------------------------------
-template <int W, int NB, int JPG, int D, bool BF>
+template <int W, int NB, int JPG, int D, bool BF, typename EXT = NoExt>
 __global__ __launch_bounds__(W * 64) void gemm_small_m_lds_kernel(GemmArgs a, int x_chunks,
-                                                                  int s_chunks, int z_chunks) {
+                                                                  int s_chunks, int z_chunks,
+                                                                  EXT ext) {
     static_assert(D >= 2 && D <= 12, "ring of 2..12 stages");
     constexpr int NG = 4 / JPG;
     constexpr int LPS = NB;  // vector-memory loads per stage: the weight blocks
@@ -666,6 +674,8 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_lds_kernel(GemmArgs a, in
         const int m0 = 4 * (l >> 4);
         if (n >= a.N)
             continue;
+        if constexpr (EXT::on)
+            lora_add4<BF>(ext.l, a.M, a.N, m0, n, v);
 #pragma unroll
         for (int rr = 0; rr < 4; rr++)
             if (m0 + rr < a.M)

@@ -174,9 +174,8 @@ int launch_dequant(const uint32_t *qp, const uint16_t *scales, const uint32_t *z
 // ---------------------------------------------------------------------------
 // GEMM dispatch
 // ---------------------------------------------------------------------------
-int launch_gemm(const uint16_t *X, const void *q_dev, const void *s_dev,
-                const void *z_dev, const Geom &geo, const GemmPlan &plan, uint16_t *Y,
-                void *workspace, void *stream) {
+GemmArgs gemm_args(const uint16_t *X, const void *q_dev, const void *s_dev, const void *z_dev,
+                   const Geom &geo, const GemmPlan &plan, uint16_t *Y, void *workspace) {
     GemmArgs a;
     a.X = X;
     a.qd = (const u4_t *)q_dev;
@@ -194,27 +193,33 @@ int launch_gemm(const uint16_t *X, const void *q_dev, const void *s_dev,
     a.sym = geo.sym ? 1 : 0;
     a.lg = __builtin_ctz((unsigned)geo.g);
     a.bf16 = geo.bf16 ? 1 : 0;
-    hipStream_t st = (hipStream_t)stream;
     a.ws = (float *)workspace;
-    a.splits = 1;
-    a.kts = a.KT;
-    if (plan.path == PATH_SMALL) {
-        SmallPlan sp;
-        sp.waves = plan.waves;
-        sp.nb = plan.nb;
-        sp.depth = plan.depth;
-        sp.mtiles = plan.mtiles;
-        sp.splits = plan.splits;
-        sp.lds = plan.lds;
-        sp.xl = plan.xl;
-        a.splits = plan.splits;
-        a.kts = (a.KT + plan.splits - 1) / plan.splits;
-        return launch_small_m(a, sp, st);
-    }
-    LargePlan lp;
-    lp.shape = plan.large_shape;
     a.splits = plan.splits;
     a.kts = (a.KT + plan.splits - 1) / plan.splits;
+    return a;
+}
+
+SmallPlan small_plan(const GemmPlan &plan) {
+    SmallPlan sp;
+    sp.waves = plan.waves;
+    sp.nb = plan.nb;
+    sp.depth = plan.depth;
+    sp.mtiles = plan.mtiles;
+    sp.splits = plan.splits;
+    sp.lds = plan.lds;
+    sp.xl = plan.xl;
+    return sp;
+}
+
+int launch_gemm(const uint16_t *X, const void *q_dev, const void *s_dev,
+                const void *z_dev, const Geom &geo, const GemmPlan &plan, uint16_t *Y,
+                void *workspace, void *stream) {
+    const GemmArgs a = gemm_args(X, q_dev, s_dev, z_dev, geo, plan, Y, workspace);
+    hipStream_t st = (hipStream_t)stream;
+    if (plan.path == PATH_SMALL)
+        return launch_small_m(a, small_plan(plan), st);
+    LargePlan lp;
+    lp.shape = plan.large_shape;
     return a.bf16 ? launch_large_m_bf16(a, lp, st) : launch_large_m(a, lp, st);
 }
 

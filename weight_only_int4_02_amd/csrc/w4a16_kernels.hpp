@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include "w4a16_device.hpp"
+#include "w4a16_internal.hpp"
 
 namespace w4a16 {
 
@@ -37,6 +38,11 @@ struct SmallPlan {
 };
 
 
+// The kernels' arguments of one call, from its geometry and plan.
+GemmArgs gemm_args(const uint16_t *X, const void *q_dev, const void *s_dev, const void *z_dev,
+                   const Geom &geo, const GemmPlan &plan, uint16_t *Y, void *workspace);
+SmallPlan small_plan(const GemmPlan &plan);
+
 int launch_small_m(const GemmArgs &a, const SmallPlan &p, hipStream_t stream);
 // Y = RNE_fp16(sum of the a.splits fp32 partial-sum slices in a.ws).
 int launch_splitk_reduce(const GemmArgs &a, hipStream_t stream);
@@ -60,5 +66,17 @@ struct LargePlan {
 
 int launch_large_m(const GemmArgs &a, const LargePlan &p, hipStream_t stream);
 int launch_large_m_bf16(const GemmArgs &a, const LargePlan &p, hipStream_t stream);
+
+// The same kernels with low-rank adapters added to their results (with a K
+// split, in slice 0).
+struct LoraExt;
+int launch_small_m_jpg1_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_small_m_jpg2_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_small_m_jpg4_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_small_m_jpg1_bf16_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_small_m_jpg2_bf16_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_small_m_jpg4_bf16_lora(const GemmArgs &a, const SmallPlan &p, const LoraExt &x, hipStream_t st);
+int launch_large_m_lora(const GemmArgs &a, const LargePlan &p, const LoraExt &x, hipStream_t st);
+int launch_large_m_bf16_lora(const GemmArgs &a, const LargePlan &p, const LoraExt &x, hipStream_t st);
 
 }  // namespace w4a16

@@ -1,0 +1,104 @@
+// Internal interface of the routed operators (include/w4a16_routed.h): plans,
+// kernel arguments and launchers.  Plain C++ (no HIP types), shared with the
+// pure-host checks.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "w4a16_internal.hpp"
+
+namespace w4a16 {
+
+// ---- routing ---------------------------------------------------------------
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int T, E, k, n_groups, topk_groups, group_top;
+    float scale;
+    int sigmoid, renormalize;
+};
+int launch_route(const RouteArgs &a, int logits_dtype, void *stream);
+
+// ---- experts ---------------------------------------------------------------
+// Rows (t, j) of the [T][k] slots are numbered flat, t k + j.  A tile is up to
+// `bm` rows of one expert.  Up to kDirectRows rows, the workgroups find their
+// tile from the ids themselves: slot y is a tile if it is the first, (bm +
+// 1)-th, ... slot of its expert.  Above, a plan kernel sorts the rows by expert
+// and lists the tiles.
+constexpr int kDirectRows = 64;
+constexpr int kMaxExperts = 1024;
+
+struct ExpertTile {
+    int32_t expert, row0, rows, unused;
+};
+
+struct ExpertsPlan {
+    int direct;          // no plan kernel
+    int mt;              // small kernel: 16-row activation tiles per workgroup
+    int bm;              // rows per tile
+    int64_t tiles;       // tiles launched (an upper bound)
+    size_t tiles_off, perm_off, h_off, p_off, ws_bytes;
+};
+ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int64_t E, int32_t g,
+                         uint32_t flags);
+
+// One grouped product.  Weight pointers are those of expert 0; `parts`
+// matrices of NT 16-row tiles for each expert.
+struct ExpertsArgs {
+    const uint16_t *X;      // 16-bit rows of K
+    const void *qd, *sd, *zd;
+    void *Y;                // gated: h, 16-bit [rows][N]; else fp32 [T k][N]
+    const int32_t *ids;     // [R]
+    const int32_t *perm;    // sorted position -> flat row (plan)
+    const ExpertTile *tiles;  // (plan)
+    int64_t x_rows;         // rows of X
+    int R, E, k, direct;
+    int N, K, g, G, GW, KT, NT, lg, sym;
+};
+
+struct CombineArgs {
+    const float *P;         // [T k][D]
+    const int32_t *ids;
+    const float *weights;
+    uint16_t *Y;            // [T][D]
+    int64_t T, D;
+    int k, E, bf16;
+};
+
+int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
+                       int32_t *perm, void *stream);
+int launch_experts_small(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
+int launch_experts_small_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
+int launch_experts_combine(const CombineArgs &a, void *stream);
+
+// ---- adapters ----------------------------------------------------------------
+constexpr int kMaxParts = 8;
+
+// What the GEMM kernels' epilogue needs to add the adapters.
+struct LoraArgs {
+    const float *S;          // [M][parts r] low-rank values, times the adapter's scale
+    const uint16_t *B;       // [n][N][r]
+    const int32_t *ids;      // [M]
+    int n, r, pr, parts;     // pr = parts r
+    int part_end[kMaxParts]; // first column after part p
+};
+struct LoraShrinkArgs {
+    const uint16_t *X, *A;
+    const float *scales;
+    const int32_t *ids;
+    float *S;
+    int64_t M;
+    int K, n, pr, bf16;
+};
+int launch_lora_shrink(const LoraShrinkArgs &a, void *stream);
+int launch_gemm_lora(const uint16_t *X, const void *q_dev, const void *s_dev, const void *z_dev,
+                     const Geom &geo, const GemmPlan &plan, const LoraArgs &lora, uint16_t *Y,
+                     void *workspace, void *stream);
+
+// w4a16_api.hip: the architecture gate and the error text of this host thread
+int32_t arch_gate();
+int32_t finish_launch(const char *what, int err);
+
+}  // namespace w4a16

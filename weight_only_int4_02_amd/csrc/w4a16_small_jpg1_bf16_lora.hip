@@ -1,0 +1,5 @@
+// Small-M kernel instances for 1 MFMA step(s) per group, bfloat16, with adapters.
+#define W4A16_JPG 1
+#define W4A16_BF 1
+#define W4A16_LORA
+#include "w4a16_small_inst.inc"

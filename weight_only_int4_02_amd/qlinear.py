@@ -17,6 +17,7 @@ from typing import Optional, Sequence
 import torch
 
 from . import PackedWeight, gemm, pack, quantize, repack
+from .lora import Adapters, gemm_lora
 
 
 class QLinear(torch.nn.Module):
@@ -58,9 +59,18 @@ class QLinear(torch.nn.Module):
         return cls(pack(codes), scales, None if zeros is None else pack(zeros), K, g,
                    bias=bias, keep_canonical=keep_canonical)
 
-    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+                adapters: Optional[Adapters] = None,
+                ids: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """adapters, ids: low-rank adapters and the adapter of each row of x
+        (int32, x's leading dimensions; -1 for none), added by gemm_lora."""
         shape = x.shape
-        y = gemm(x.reshape(-1, self.K), self.packed, out=out)
+        if (adapters is None) != (ids is None):
+            raise ValueError("adapters and ids go together")
+        if adapters is None:
+            y = gemm(x.reshape(-1, self.K), self.packed, out=out)
+        else:
+            y = gemm_lora(x.reshape(-1, self.K), self.packed, adapters, ids.reshape(-1), out=out)
         if self.bias is not None:
             y.add_(self.bias)   # in place: a caller's `out` holds the result
         return y.reshape(*shape[:-1], self.N)
@@ -75,8 +85,11 @@ class FusedQLinear(torch.nn.Module):
         self.fused = fused
         self.sizes = list(sizes)
 
-    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None):
-        y = self.fused(x, out=out)
+    def forward(self, x: torch.Tensor, out: Optional[torch.Tensor] = None,
+                adapters: Optional[Adapters] = None, ids: Optional[torch.Tensor] = None):
+        """adapters (lora.adapters with this layer's sizes: an A for each part)
+        and ids as QLinear's."""
+        y = self.fused(x, out=out, adapters=adapters, ids=ids)
         return torch.split(y, self.sizes, dim=-1)
 
 
