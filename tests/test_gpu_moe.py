@@ -142,6 +142,11 @@ CASES = [
     (7, 4, 2, 512, 256, 257, 64), (16, 4, 4, 256, 384, 256, 32), (64, 2, 1, 136, 72, 17, 32),
     (33, 8, 2, 520, 200, 264, 256), (40, 2, 2, 256, 264, 256, 128), (100, 16, 4, 384, 128, 130, 128),
     (200, 3, 1, 1024, 104, 64, 64), (300, 4, 4, 256, 256, 512, 128),
+    # the compute-bound kernel: 64-row and 128-row tiles, every group size,
+    # K of one, few and many stages, ragged columns and a partial last stage
+    (130, 8, 2, 128, 136, 257, 32), (150, 6, 2, 392, 512, 260, 64), (129, 4, 1, 648, 72, 300, 256),
+    (333, 2, 1, 264, 640, 516, 32), (257, 3, 3, 1160, 264, 131, 64), (500, 2, 1, 512, 1032, 640, 256),
+    (140, 1, 1, 128, 128, 16, 128), (700, 5, 2, 640, 200, 1100, 128),
 ]
 
 

@@ -1,0 +1,3 @@
+// The experts' large products, bfloat16.
+#define W4A16_BF 1
+#include "w4a16_experts_large.inc"

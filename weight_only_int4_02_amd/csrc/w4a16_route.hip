@@ -232,6 +232,7 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
                                                                    int R, int E, int bm,
                                                                    int tiles_max,
                                                                    ExpertTile *__restrict__ tiles,
+                                                                   int32_t *__restrict__ tiles_used,
                                                                    int32_t *__restrict__ perm) {
     __shared__ int count[kMaxExperts];
     __shared__ int part[kPlanThreads / 64][3];
@@ -271,10 +272,14 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
     const int mine = count[e];
     for (int i = tid; i * bm < mine; i += kPlanThreads)
         if (tile0 + i < tiles_max)
-            tiles[tile0 + i] = ExpertTile{e, row0 + i * bm, min(bm, mine - i * bm), 0};
-    if (e == E - 1)
+            tiles[tile0 + i] = ExpertTile{e,     row0 + i * bm,         min(bm, mine - i * bm),
+                                          tile0, (mine + bm - 1) / bm,  {0, 0, 0}};
+    if (e == E - 1) {
         for (int i = used + tid; i < tiles_max; i += kPlanThreads)
-            tiles[i] = ExpertTile{0, 0, 0, 0};
+            tiles[i] = ExpertTile{0, 0, 0, 0, 0, {0, 0, 0}};
+        if (tid == 0)
+            *tiles_used = used;
+    }
     if (mine == 0)
         return;
     int at = row0;
@@ -367,9 +372,9 @@ int launch_route(const RouteArgs &a, int logits_dtype, void *stream) {
 }
 
 int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
-                       int32_t *perm, void *stream) {
+                       int32_t *tiles_used, int32_t *perm, void *stream) {
     hipLaunchKernelGGL(expert_plan_kernel, dim3((unsigned)E), dim3(kPlanThreads), 0,
-                       (hipStream_t)stream, ids, R, E, bm, tiles_max, tiles, perm);
+                       (hipStream_t)stream, ids, R, E, bm, tiles_max, tiles, tiles_used, perm);
     return (int)hipGetLastError();
 }
 

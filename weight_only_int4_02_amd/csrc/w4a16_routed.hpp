@@ -31,15 +31,18 @@ constexpr int kDirectRows = 64;
 constexpr int kMaxExperts = 1024;
 
 struct ExpertTile {
-    int32_t expert, row0, rows, unused;
+    int32_t expert, row0, rows;   // rows row0 .. of the sorted order
+    int32_t first, count;         // the expert's tiles: first .. first + count - 1
+    int32_t unused[3];
 };
 
 struct ExpertsPlan {
     int direct;          // no plan kernel
+    int large;           // the compute-bound kernel
     int mt;              // small kernel: 16-row activation tiles per workgroup
     int bm;              // rows per tile
     int64_t tiles;       // tiles launched (an upper bound)
-    size_t tiles_off, perm_off, h_off, p_off, ws_bytes;
+    size_t used_off, tiles_off, perm_off, h_off, p_off, ws_bytes;
 };
 ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int64_t E, int32_t g,
                          uint32_t flags);
@@ -53,6 +56,7 @@ struct ExpertsArgs {
     const int32_t *ids;     // [R]
     const int32_t *perm;    // sorted position -> flat row (plan)
     const ExpertTile *tiles;  // (plan)
+    const int32_t *tiles_used;  // (plan) how many
     int64_t x_rows;         // rows of X
     int R, E, k, direct;
     int N, K, g, G, GW, KT, NT, lg, sym;
@@ -68,9 +72,11 @@ struct CombineArgs {
 };
 
 int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
-                       int32_t *perm, void *stream);
+                       int32_t *tiles_used, int32_t *perm, void *stream);
 int launch_experts_small(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_small_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
+int launch_experts_large(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
+int launch_experts_large_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_combine(const CombineArgs &a, void *stream);
 
 // ---- adapters ----------------------------------------------------------------

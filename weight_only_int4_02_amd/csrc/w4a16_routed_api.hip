@@ -81,6 +81,7 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
     const ExpertsPlan p = plan_experts(T, k, K, I, D, E, g, flags);
     char *ws = (char *)workspace;
     ExpertTile *tiles = (ExpertTile *)(ws + p.tiles_off);
+    int32_t *used = (int32_t *)(ws + p.used_off);
     int32_t *perm = (int32_t *)(ws + p.perm_off);
     uint16_t *h = (uint16_t *)(ws + p.h_off);
     float *P = (float *)(ws + p.p_off);
@@ -88,7 +89,7 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
     const bool bf = (flags & W4A16_BF16) != 0;
     int e = 0;
     if (!p.direct)
-        e = launch_expert_plan(ids, R, (int)E, p.bm, (int)p.tiles, tiles, perm, stream);
+        e = launch_expert_plan(ids, R, (int)E, p.bm, (int)p.tiles, tiles, used, perm, stream);
     ExpertsArgs gu = product(X, T, K, gate_up_q, gate_up_s, gate_up_z, I, g, flags);
     ExpertsArgs dn = product(h, R, I, down_q, down_s, down_z, D, g, flags);
     gu.Y = h;
@@ -97,14 +98,18 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
         a->ids = ids;
         a->perm = perm;
         a->tiles = tiles;
+        a->tiles_used = used;
         a->R = R;
         a->E = (int)E;
         a->k = k;
         a->direct = p.direct;
     }
-    for (int gated = 1; gated >= 0 && !e; gated--)
-        e = bf ? launch_experts_small_bf16(gated ? gu : dn, p, gated != 0, stream)
-               : launch_experts_small(gated ? gu : dn, p, gated != 0, stream);
+    const auto launch = p.large ? (bf ? launch_experts_large_bf16 : launch_experts_large)
+                                : (bf ? launch_experts_small_bf16 : launch_experts_small);
+    if (!e)
+        e = launch(gu, p, true, stream);
+    if (!e)
+        e = launch(dn, p, false, stream);
     if (!e) {
         CombineArgs c;
         c.P = P;

@@ -42,7 +42,7 @@ int32_t check_experts_shape(int64_t T, int32_t k, int64_t K, int64_t I, int64_t 
         dn.NT * dn.KT * 1024 >= (int64_t(1) << 31) || T * K * 2 >= (int64_t(1) << 31))
         return W4A16_ERR_SHAPE;
     // a tile's h rows too
-    if (64 * I * 2 >= (int64_t(1) << 31))
+    if (128 * I * 2 >= (int64_t(1) << 31))
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
@@ -59,8 +59,9 @@ int32_t check_lora_shape(int64_t N, int64_t K, int64_t n, int32_t r, int32_t n_p
 
 }  // namespace
 
-// Rows per tile: 16 (one MFMA row tile) while an expert has few rows on
-// average, 64 above.
+// Rows per tile: 16 (one MFMA row tile, the memory-bound kernel) while an
+// expert has few rows on average, then 64 and 128 rows of the compute-bound
+// kernel.
 ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int64_t E, int32_t g,
                          uint32_t flags) {
     ExpertsPlan p;
@@ -70,11 +71,14 @@ ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int6
     const int64_t R = T * k;
     p.direct = R <= kDirectRows;
     p.mt = R <= 16 * E ? 1 : 4;
-    p.bm = 16 * p.mt;
+    p.large = !p.direct && R > 16 * E;
+    p.bm = !p.large ? 16 * p.mt : R <= 64 * E ? 64 : 128;
     // sum over the experts with rows of ceil(rows / bm), at most
     const int64_t used = R < E ? R : E;
     p.tiles = p.direct ? R : used + (R - used) / p.bm;
     size_t at = 0;
+    p.used_off = at;
+    at += p.direct ? 0 : 256;
     p.tiles_off = at;
     at += p.direct ? 0 : up256((size_t)p.tiles * sizeof(ExpertTile));
     p.perm_off = at;
