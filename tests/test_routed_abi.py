@@ -113,11 +113,21 @@ def gemm_lora(sizes=(256, 256), **kw):
     (dict(X=None), w4.ERR_NULL), (dict(z=None), w4.ERR_NULL), (dict(M=0), w4.ERR_SHAPE),
     (dict(K=500), w4.ERR_SHAPE), (dict(g=100), w4.ERR_GROUP), (dict(A=P(8)), w4.ERR_ALIGN),
     (dict(B=P(2)), w4.ERR_ALIGN), (dict(scales=P(2)), w4.ERR_ALIGN), (dict(ids=P(1)), w4.ERR_ALIGN),
-    (dict(ws=P(4)), w4.ERR_ALIGN), (dict(wsb=511), w4.ERR_WORKSPACE), (dict(wsb=512), w4.OK),
+    (dict(ws=P(4)), w4.ERR_ALIGN), (dict(wsb=16), w4.ERR_WORKSPACE),
     (dict(Y=P()), w4.ERR_SHAPE), (dict(ids=P(1 << 31)), w4.ERR_SHAPE), (dict(flags=0x400), w4.ERR_FLAGS),
 ])
 def test_gemm_lora_args(kw, status):
     assert gemm_lora(**kw) == status
+
+
+def test_gemm_lora_workspace_is_what_the_check_asks_for():
+    for M, r in ((1, 8), (4, 16), (33, 40), (700, 256)):
+        b = ctypes.c_size_t()
+        assert lora._routed().w4a16_gemm_lora_workspace_size(M, 512, 512, 128, 0, 2, r, ctypes.byref(b)) == w4.OK
+        assert b.value >= w4.workspace_size(M, 512, 512, 128, 0) + M * 2 * r * 4
+        assert gemm_lora(M=M, r=r, wsb=b.value) == w4.OK
+        assert gemm_lora(M=M, r=r, wsb=b.value - 1) == w4.ERR_WORKSPACE
+    assert lora._routed().w4a16_gemm_lora_workspace_size(1, 512, 512, 128, 0, 2, 16, None) == w4.ERR_NULL
 
 
 def test_binding_refuses_what_it_cannot_take():

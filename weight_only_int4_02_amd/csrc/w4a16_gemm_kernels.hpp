@@ -101,6 +101,15 @@ __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t rsrc, u4_t *lds
         rsrc, (__attribute__((address_space(3))) void *)lds_wave_base, 16, (int)voffset, 0, 0, 0);
 }
 
+// The same with a wave-uniform part of the offset in a scalar register (the
+// per-lane part carries the range check).
+__device__ __forceinline__ void lds_dma16_so(__amdgpu_buffer_rsrc_t rsrc, u4_t *lds_wave_base,
+                                             uint32_t voffset, uint32_t soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        rsrc, (__attribute__((address_space(3))) void *)lds_wave_base, 16, (int)voffset,
+        (int)soffset, 0, 0);
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
     static_assert(N >= 0 && N < 64, "vmcnt counts 0..63");
@@ -359,8 +368,7 @@ __device__ __forceinline__ void small_wait(int after) {
     }
 }
 
-// EXT: what is added to the fp32 results before they are rounded (LoraExt), or
-// nothing (NoExt).
+// EXT: what is added to the fp32 accumulators (LoraExt), or nothing (NoExt).
 template <int W, int NB, int MT, int JPG, int D, bool BF, bool XL = false, typename EXT = NoExt>
 __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a, EXT ext) {
     static_assert(D >= 2 && D <= 12, "ring of 2..12 stages");
@@ -442,11 +450,47 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a, EXT ex
         else
             return nullptr;
     };
+    // An extension's first loads go out before the ring's, and it is added
+    // while the first stages are in flight; where registers leave no room for
+    // both, before them (the widest shape: after the last).
+    constexpr bool kLast = NB == 8 && XL;
+    constexpr bool kRoom = XL ? NB * MT <= 6 : MT == 1 && W <= 8;
+    auto with_ext = [&](auto &&between) __attribute__((always_inline)) {
+        if constexpr (EXT::on) {
+            const int l = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+            auto add = [&](auto p_c) __attribute__((always_inline)) {
+                LoraPart<BF, W, NB, MT, decltype(p_c)::value> part(ext.l, a.M, a.N, m_base, nt0 * 16,
+                                                                   wave, l);
+                part.begin();
+                between();
+                part.finish(acc);
+            };
+            // (pairs of rank blocks where their registers fit)
+            constexpr int P = NB < 8 && W < 16 ? 2 : 1;
+            if (blockIdx.z != 0)
+                between();
+            else if (P == 1 || ext.l.blocks == 1)
+                add(std::integral_constant<int, 1>{});
+            else
+                add(std::integral_constant<int, P>{});
+        }
+    };
+    if constexpr (EXT::on && !kRoom && !kLast)
+        with_ext([]() {});
     Stage st[D];
+    if constexpr (EXT::on && kRoom) {
+        with_ext([&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int p = 0; p < D - 1; p++)
-        if (p < S)
-            small_issue<false>(st[p], a, d, o, tile(p), i, xl, p);
+            for (int p = 0; p < D - 1; p++)
+                if (p < S)
+                    small_issue<false>(st[p], a, d, o, tile(p), i, xl, p);
+        });
+    } else {
+#pragma unroll
+        for (int p = 0; p < D - 1; p++)
+            if (p < S)
+                small_issue<false>(st[p], a, d, o, tile(p), i, xl, p);
+    }
     auto step = [&](int s, auto slot_c) __attribute__((always_inline)) {
         constexpr int slot = decltype(slot_c)::value;
         if (s + D - 1 < S)
@@ -465,14 +509,24 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a, EXT ex
         small_compute<BF>(st[0], a, KTF, magic, acc, xslot(0), r, i);
     }
 
+    if constexpr (EXT::on && kLast)
+        with_ext([]() {});
+    // with an extension, the lane and thread number are formed anew rather than
+    // held through the main loop, where the widest shape has no register left
+    // for them
+    int lane_e = lane, tid_e = threadIdx.x;
+    if constexpr (EXT::on) {
+        lane_e = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+        tid_e = wave * 64 + lane_e;
+    }
 #pragma unroll
     for (int b = 0; b < NB; b++)
 #pragma unroll
         for (int t = 0; t < MT; t++)
-            ((f4_t *)(smem + wave * PW))[(b * MT + t) * 64 + lane] = acc[b][t];
+            ((f4_t *)(smem + wave * PW))[(b * MT + t) * 64 + lane_e] = acc[b][t];
     __syncthreads();
     constexpr int SLOTS = NB * MT * 64;
-    for (int idx = threadIdx.x; idx < SLOTS; idx += W * 64) {
+    for (int idx = tid_e; idx < SLOTS; idx += W * 64) {
         const int b = idx / (MT * 64), t = (idx / 64) % MT, l = idx & 63;
         f4_t v = ((const f4_t *)smem)[(b * MT + t) * 64 + l];
 #pragma unroll
@@ -482,10 +536,6 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_kernel(GemmArgs a, EXT ex
         const int m0 = m_base + t * 16 + 4 * (l >> 4);
         if (n >= a.N)
             continue;
-        if constexpr (EXT::on) {
-            if (blockIdx.z == 0)
-                lora_add4<BF>(ext.l, a.M, a.N, m0, n, v);
-        }
         if (a.splits == 1) {
 #pragma unroll
             for (int rr = 0; rr < 4; rr++) {
@@ -551,6 +601,22 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_lds_kernel(GemmArgs a, in
                           (uint32_t)((c - x_chunks - s_chunks) * 1024 + lane * 16));
         }
     }
+    // (an extension's loads are in flight beside these copies)
+    f4_t low[NB][1];
+    if constexpr (EXT::on) {
+#pragma unroll
+        for (int b = 0; b < NB; b++)
+            low[b][0] = f4_t{0.f, 0.f, 0.f, 0.f};
+        auto add = [&](auto p_c) __attribute__((always_inline)) {
+            LoraPart<BF, W, NB, 1, decltype(p_c)::value> part(ext.l, a.M, a.N, 0, nt0 * 16, wave, lane);
+            part.begin();
+            part.finish(low);
+        };
+        if (ext.l.blocks == 1)
+            add(std::integral_constant<int, 1>{});
+        else
+            add(std::integral_constant<int, 2>{});
+    }
     const uint16_t *s_lds = (const uint16_t *)&lds[x_chunks * 64];
     const uint32_t *z_lds = (const uint32_t *)&lds[(x_chunks + s_chunks) * 64];
     const int xrow = r < a.M ? r : a.M - 1;
@@ -567,7 +633,7 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_lds_kernel(GemmArgs a, in
     f4_t acc[NB];
 #pragma unroll
     for (int b = 0; b < NB; b++)
-        acc[b] = f4_t{0.f, 0.f, 0.f, 0.f};
+        acc[b] = EXT::on ? low[b][0] : f4_t{0.f, 0.f, 0.f, 0.f};
 
     const int KTF = a.K >> 7;
     const int S = KTF > wave ? (KTF - wave + W - 1) / W : 0;
@@ -674,8 +740,6 @@ __global__ __launch_bounds__(W * 64) void gemm_small_m_lds_kernel(GemmArgs a, in
         const int m0 = 4 * (l >> 4);
         if (n >= a.N)
             continue;
-        if constexpr (EXT::on)
-            lora_add4<BF>(ext.l, a.M, a.N, m0, n, v);
 #pragma unroll
         for (int rr = 0; rr < 4; rr++)
             if (m0 + rr < a.M)

@@ -82,21 +82,43 @@ int launch_experts_combine(const CombineArgs &a, void *stream);
 // ---- adapters ----------------------------------------------------------------
 constexpr int kMaxParts = 8;
 
-// What the GEMM kernels' epilogue needs to add the adapters.
+// The low-rank values S of every row, in blocks of 32 ranks of one part (the
+// last block of a part filled up with zeros): hi + lo in the 16-bit type,
+// [parts blocks][M][32] each, and (fp16) the rows' factors [parts blocks][f_pitch].
+// The distinct adapters of each 16-row tile are listed too.
+struct LoraList {
+    int32_t count, unused[3];
+    int32_t adapter[16];
+    uint32_t rows[16];       // bit j: row j of the tile names it
+};
+struct LoraPlan {
+    int blocks;              // of 32 ranks, per part
+    int lanes;               // first product: workgroups for the adapters of a row tile
+    int64_t f_pitch;         // M in whole row tiles
+    size_t s_hi_off, s_lo_off, f_off, bytes;   // (the lists come first)
+};
+LoraPlan plan_lora(int64_t M, int parts, int r, bool bf16);
+
+// What the GEMM kernels need to add the adapters.
 struct LoraArgs {
-    const float *S;          // [M][parts r] low-rank values, times the adapter's scale
+    const uint16_t *S_hi, *S_lo;
+    const float *F;
+    const LoraList *lists;   // [row tiles]
     const uint16_t *B;       // [n][N][r]
     const int32_t *ids;      // [M]
-    int n, r, pr, parts;     // pr = parts r
+    int64_t f_pitch;
+    int n, r, blocks, parts;
     int part_end[kMaxParts]; // first column after part p
 };
 struct LoraShrinkArgs {
-    const uint16_t *X, *A;
+    const uint16_t *X, *A;   // A [n][parts r][K]
     const float *scales;
     const int32_t *ids;
-    float *S;
-    int64_t M;
-    int K, n, pr, bf16;
+    uint16_t *S_hi, *S_lo;
+    float *F;
+    LoraList *lists;
+    int64_t M, f_pitch;
+    int K, n, r, parts, blocks, lanes, bf16;
 };
 int launch_lora_shrink(const LoraShrinkArgs &a, void *stream);
 int launch_gemm_lora(const uint16_t *X, const void *q_dev, const void *s_dev, const void *z_dev,

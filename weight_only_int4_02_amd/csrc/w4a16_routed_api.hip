@@ -142,25 +142,37 @@ int32_t w4a16_gemm_lora(const uint16_t *X, int64_t M, int64_t K, const void *q_d
     (void)hipGetLastError();
     const Geom geo = make_geom(M, N, K, g, flags);
     const GemmPlan plan = plan_gemm(geo, flags);
-    float *S = (float *)((char *)workspace + ((plan.ws_bytes + 255) & ~(size_t)255));
+    const LoraPlan lp = plan_lora(M, n_parts, r, geo.bf16);
+    char *ws = (char *)workspace + ((plan.ws_bytes + 255) & ~(size_t)255);
     LoraShrinkArgs sh;
     sh.X = X;
     sh.A = A;
     sh.scales = scales;
     sh.ids = adapter_ids;
-    sh.S = S;
+    sh.lists = (LoraList *)ws;
+    sh.S_hi = (uint16_t *)(ws + lp.s_hi_off);
+    sh.S_lo = (uint16_t *)(ws + lp.s_lo_off);
+    sh.F = (float *)(ws + lp.f_off);
     sh.M = M;
+    sh.f_pitch = lp.f_pitch;
     sh.K = (int)K;
     sh.n = (int)n;
-    sh.pr = n_parts * r;
+    sh.r = r;
+    sh.parts = n_parts;
+    sh.blocks = lp.blocks;
+    sh.lanes = lp.lanes;
     sh.bf16 = geo.bf16 ? 1 : 0;
     LoraArgs lo;
-    lo.S = S;
+    lo.S_hi = sh.S_hi;
+    lo.S_lo = sh.S_lo;
+    lo.F = sh.F;
     lo.B = B;
+    lo.lists = sh.lists;
     lo.ids = adapter_ids;
     lo.n = (int)n;
+    lo.f_pitch = lp.f_pitch;
     lo.r = r;
-    lo.pr = n_parts * r;
+    lo.blocks = lp.blocks;
     lo.parts = n_parts;
     int64_t end = 0;
     for (int p = 0; p < kMaxParts; p++) {

@@ -91,6 +91,23 @@ ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int6
     return p;
 }
 
+// Up to 16 row tiles, each adapter of a tile has a workgroup in the first
+// product, above two share them (see lora_shrink_kernel): one for most tiles
+// of a prompt, the second for those where two prompts meet (six prompts at M =
+// 2048, K = 11008: 29.7 us with one, 17.1 for a single prompt).
+LoraPlan plan_lora(int64_t M, int parts, int r, bool bf16) {
+    LoraPlan p;
+    p.blocks = (r + 31) / 32;
+    p.lanes = M > 256 ? 2 : M < 16 ? (int)M : 16;
+    p.f_pitch = (M + 15) / 16 * 16;
+    const size_t values = (size_t)parts * (size_t)p.blocks * (size_t)M * 32 * 2;
+    p.s_hi_off = up256((size_t)(p.f_pitch / 16) * sizeof(LoraList));
+    p.s_lo_off = p.s_hi_off + up256(values);
+    p.f_off = p.s_lo_off + up256(values);
+    p.bytes = p.f_off + (bf16 ? 0 : (size_t)parts * (size_t)p.blocks * (size_t)p.f_pitch * 4);
+    return p;
+}
+
 }  // namespace w4a16
 
 using namespace w4a16;
@@ -167,7 +184,7 @@ int32_t w4a16_gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t 
         st = check_lora_shape(N, K, 1, r, n_parts);
     if (st)
         return st;
-    *bytes = up256(gemm) + (size_t)M * (size_t)n_parts * (size_t)r * 4;
+    *bytes = up256(gemm) + plan_lora(M, n_parts, r, (flags & W4A16_BF16) != 0).bytes;
     return W4A16_OK;
 }
 
