@@ -16,9 +16,9 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import (BF16, PATH_LARGE_M, PATH_SMALL_M, PackedWeight, _check_packed, _need, _need16,
-               _raise, lib)
-from .moe import _at, on_current_device
+from . import (BF16, PATH_LARGE_M, PATH_SMALL_M, SYMMETRIC, PackedWeight, _need, _need16, _raise,
+               lib)
+from .moe import _at, check, device_layout_bytes, stream_of
 
 MAX_PARTS = 8
 MAX_RANK = 256
@@ -75,8 +75,9 @@ def adapters(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor,
     A[:, p].  A rank that is no multiple of 8 is padded with zeros (a copy), and
     adapters of smaller rank may be padded with zeros up to r."""
     bf = _need16(A, "A")
-    _need(B, "B", torch.bfloat16 if bf else torch.float16, 3)
-    _need(scales, "scales", torch.float32, 1)
+    device = A.get_device()
+    check(B, "B", torch.bfloat16 if bf else torch.float16, 3, device)
+    check(scales, "scales", torch.float32, 1, device)
     if A.dim() == 3:
         A = A.unsqueeze(1)
     if A.dim() != 4:
@@ -90,7 +91,6 @@ def adapters(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor,
         raise ValueError("B must be [n, N, r] and scales [n]")
     if r < 1 or r > MAX_RANK:
         raise ValueError(f"a rank of 1 to {MAX_RANK}")
-    on_current_device(A, B, scales)
     if r % 8:
         pad = 8 - r % 8
         A = torch.cat([A, A.new_zeros((n, parts, pad, K))], 2)
@@ -120,18 +120,21 @@ def gemm_lora(X: torch.Tensor, w: PackedWeight, ad: Adapters, ids: torch.Tensor,
     torch's allocator (so calls on other streams, and captured ones, have
     their own)."""
     bf = _need16(X, "X", 2)
-    _need(ids, "ids", torch.int32, 1)
+    device, dtype = X.get_device(), X.dtype
+    check(ids, "ids", torch.int32, 1, device)
     M, K = X.shape
-    if K != w.K or w.K != ad.A.shape[2] or w.N != ad.B.shape[1]:
-        raise ValueError(f"X has K={K}, the weight is [{w.N}, {w.K}], the adapters [{ad.N}, {ad.K}]")
-    if bf != bool(w.flags & BF16) or X.dtype != ad.A.dtype:
+    N = w.N
+    if K != w.K or w.K != ad.A.shape[2] or N != ad.B.shape[1]:
+        raise ValueError(f"X has K={K}, the weight is [{N}, {w.K}], the adapters [{ad.N}, {ad.K}]")
+    if bf != bool(w.flags & BF16):
         raise TypeError("X, the weight's scales and the adapters must share one 16-bit format")
     if ids.shape[0] != M:
         raise ValueError("ids must be [M]")
-    n, pr = ad.n, len(ad.sizes) * ad.r
-    if tuple(ad.A.shape) != (n, pr, K) or tuple(ad.B.shape) != (n, w.N, ad.r) or \
-            ad.B.dtype != X.dtype or tuple(ad.scales.shape) != (n,) or \
-            not (ad.A.is_contiguous() and ad.B.is_contiguous()):
+    n, r, parts = ad.n, ad.r, len(ad.sizes)
+    check(ad.A, "adapters.A", dtype, 3, device)
+    check(ad.B, "adapters.B", dtype, 3, device)
+    check(ad.scales, "adapters.scales", torch.float32, 1, device)
+    if ad.A.shape != (n, parts * r, K) or ad.B.shape != (n, N, r) or ad.scales.shape[0] != n:
         raise ValueError("the adapters' tensors do not have the shapes they need (use adapters())")
     flags = w.flags
     if path == "small_m":
@@ -140,22 +143,30 @@ def gemm_lora(X: torch.Tensor, w: PackedWeight, ad: Adapters, ids: torch.Tensor,
         flags |= PATH_LARGE_M
     elif path is not None:
         raise ValueError("path must be None, 'small_m' or 'large_m'")
-    _check_packed(w)
+    # the weight's tensors hold the bytes its shape needs
+    qb, sb, zb = device_layout_bytes(N, K, w.g)
+    check(w.q, "w.q", torch.uint8, w.q.dim(), device)
+    check(w.s, "w.s", dtype, w.s.dim(), device)
+    small = w.q.numel() < qb or w.s.numel() * 2 < sb
+    if not flags & SYMMETRIC:
+        check(w.z, "w.z", torch.int32, w.z.dim(), device)
+        small = small or w.z.numel() * 4 < zb
+    if small:
+        raise ValueError("PackedWeight tensors are smaller than its shape needs")
     if out is None:
-        out = torch.empty((M, w.N), dtype=X.dtype, device=X.device)
+        out = X.new_empty((M, N))
     else:
-        _need(out, "out", X.dtype, 2)
-        if tuple(out.shape) != (M, w.N):
+        check(out, "out", dtype, 2, device)
+        if tuple(out.shape) != (M, N):
             raise ValueError("out must be [M, N]")
+    stream = stream_of(device)
     if workspace is None:
-        workspace = torch.empty(gemm_lora_workspace_size(M, w, ad, flags), dtype=torch.uint8,
-                                device=X.device)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous device tensor")
-    stream = on_current_device(X, ids, w.q, w.s, w.z, ad.A, ad.B, ad.scales, out, workspace)
+        workspace = ids.new_empty((gemm_lora_workspace_size(M, w, ad, flags) + 3) // 4)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
     _raise(_routed().w4a16_gemm_lora(
-        X.data_ptr(), M, K, w.q.data_ptr(), w.s.data_ptr(), _at(w.z), w.N, w.g, flags,
-        ad.A.data_ptr(), ad.B.data_ptr(), ad.scales.data_ptr(), n, ad.r, len(ad.sizes), ad.c_sizes,
+        X.data_ptr(), M, K, w.q.data_ptr(), w.s.data_ptr(), _at(w.z), N, w.g, flags,
+        ad.A.data_ptr(), ad.B.data_ptr(), ad.scales.data_ptr(), n, r, parts, ad.c_sizes,
         ids.data_ptr(), out.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), stream), "w4a16_gemm_lora")
     return out

@@ -53,14 +53,35 @@ def _routed():
     return _bound
 
 
-def on_current_device(*tensors) -> int:
-    """The tensors are on the current device (whose current stream the
-    kernels are enqueued on); returns that stream."""
-    index = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != index:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{index}")
-    return torch.cuda.current_stream().cuda_stream
+def check(t, name: str, dtype, ndim: int, device: int) -> None:
+    """_need() for a tensor that must be on the call's device: one small
+    function, since a decode step's calls are made of its cost."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device} like the call's first tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions")
+
+
+def stream_of(device: int) -> int:
+    """The current stream of the current device, which must be `device`: the
+    kernels are enqueued on it."""
+    if device != torch.cuda.current_device():
+        raise ValueError(f"tensors on cuda:{device}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def device_layout_bytes(N: int, K: int, g: int):
+    """Bytes of q, s and z of one [N, K] matrix in the device layout
+    (repack_size() without its checks, which the call itself makes)."""
+    nt, G = (N + 15) // 16, -(-K // g)
+    return nt * ((K + 127) // 128) * 1024, nt * G * 32, nt * ((G + 7) // 8) * 64
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -86,14 +107,15 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax",
     if not isinstance(logits, torch.Tensor) or logits.dtype not in _LOGITS:
         raise TypeError("logits must be a float16, bfloat16 or float32 tensor")
     _need(logits, "logits", logits.dtype, 2)
+    device = logits.get_device()
     if score not in ("softmax", "sigmoid"):
         raise ValueError("score must be 'softmax' or 'sigmoid'")
     T, E = logits.shape
     if bias is not None:
-        _need(bias, "bias", torch.float32, 1)
+        check(bias, "bias", torch.float32, 1, device)
         if bias.shape[0] != E:
             raise ValueError("bias must be [E]")
-    stream = on_current_device(logits, bias)
+    stream = stream_of(device)
     # (the library's checks hold for the empty call too)
     if T == 0:
         _raise(_routed().w4a16_check_route_args(16, _LOGITS[logits.dtype], 1, E, _at(bias), k,
@@ -146,7 +168,7 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     parts = 2 if gated else 1
     if N % parts:
         raise ValueError("a gated weight has an even number of rows")
-    on_current_device(codes, scales, zeros)
+    stream_of(codes.get_device())
     n = N // parts
     flags = (SYMMETRIC if zeros is None else 0) | (PARTIAL_LAST_GROUP if K % g else 0) | (BF16 if bf else 0)
     m = E * parts
@@ -173,16 +195,16 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     return ExpertWeight(q, s, z, E, n, K, g, flags, gated)
 
 
-def _check_expert_weight(w: ExpertWeight, name: str) -> None:
+def _check_expert_weight(w: ExpertWeight, name: str, device: int) -> None:
     """The device-layout tensors hold the bytes the shape needs (the kernels
     read them through bare pointers)."""
-    qb, sb, zb = repack_size(w.N, w.K, w.g, w.flags)
+    qb, sb, zb = device_layout_bytes(w.N, w.K, w.g)
     m = w.E * (2 if w.gated else 1)
-    _need(w.q, f"{name}.q", torch.uint8)
-    _need(w.s, f"{name}.s", torch.bfloat16 if w.flags & BF16 else torch.float16)
+    check(w.q, name, torch.uint8, w.q.dim(), device)
+    check(w.s, name, torch.bfloat16 if w.flags & BF16 else torch.float16, w.s.dim(), device)
     small = w.q.numel() < m * qb or w.s.numel() * 2 < m * sb
     if not w.flags & SYMMETRIC:
-        _need(w.z, f"{name}.z", torch.int32)
+        check(w.z, name, torch.int32, w.z.dim(), device)
         small = small or w.z.numel() * 4 < m * zb
     if small:
         raise ValueError(f"{name} tensors are smaller than its shape needs")
@@ -211,8 +233,9 @@ def experts(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: 
     manage their own; without one, each call takes a new block of torch's
     allocator (so calls on other streams, and captured ones, have their own)."""
     bf = _need16(X, "X", 2)
-    _need(ids, "ids", torch.int32, 2)
-    _need(weights, "weights", torch.float32, 2)
+    device = X.get_device()
+    check(ids, "ids", torch.int32, 2, device)
+    check(weights, "weights", torch.float32, 2, device)
     T, K = X.shape
     if not gate_up.gated or down.gated:
         raise ValueError("gate_up must be a gated ExpertWeight and down a plain one")
@@ -222,25 +245,24 @@ def experts(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: 
     if (gate_up.flags ^ down.flags) & (SYMMETRIC | BF16) or bf != bool(gate_up.flags & BF16):
         raise TypeError("X, gate_up and down must share a 16-bit format, and the weights symmetry")
     k = ids.shape[1]
-    if tuple(ids.shape) != (T, k) or tuple(weights.shape) != (T, k):
+    if ids.shape[0] != T or weights.shape != ids.shape:
         raise ValueError("ids and weights must be [T, k]")
-    _check_expert_weight(gate_up, "gate_up")
-    _check_expert_weight(down, "down")
+    _check_expert_weight(gate_up, "gate_up", device)
+    _check_expert_weight(down, "down", device)
     if out is None:
-        out = torch.empty((T, down.N), dtype=X.dtype, device=X.device)
+        out = X.new_empty((T, down.N))
     else:
-        _need(out, "out", X.dtype, 2)
+        check(out, "out", X.dtype, 2, device)
         if tuple(out.shape) != (T, down.N):
             raise ValueError("out must be [T, D]")
+    stream = stream_of(device)
     need = experts_workspace_size(max(T, 1), k, gate_up, down)
-    if workspace is None:
-        workspace = torch.empty(need if T else 0, dtype=torch.uint8, device=X.device)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous device tensor")
-    stream = on_current_device(X, ids, weights, gate_up.q, gate_up.s, gate_up.z, down.q, down.s,
-                               down.z, out, workspace)
     if T == 0:
         return out
+    if workspace is None:
+        workspace = ids.new_empty(need // 4)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the call's device")
     _raise(_routed().w4a16_experts(
         X.data_ptr(), T, K, ids.data_ptr(), weights.data_ptr(), k, gate_up.E, gate_up.q.data_ptr(),
         gate_up.s.data_ptr(), _at(gate_up.z), gate_up.N, down.q.data_ptr(), down.s.data_ptr(),
