@@ -80,9 +80,11 @@ def experts(X, ids, weights, gate_up, down, g):
     [E, D, I], scales, zeros).
 
     Bound: gate and up are 32-bit sums of K products; silu's slope is at most
-    1.1 and its own arithmetic good to 8 steps; h is rounded to 16 bits (or to
-    the smallest subnormal's half); the down product adds I products, the
-    weighted sum k; the result is rounded to 16 bits."""
+    1.1 and its own arithmetic, v / (1 + exp(-v)) with exp2's argument and each
+    of the exponential, sum, quotient and product rounded, is off by at most
+    (2 |v| + 8) 2^-24 of it; h is rounded to 16 bits (or to the smallest
+    subnormal's half); the down product adds I products, the weighted sum k;
+    the result is rounded to 16 bits."""
     dt = X.dtype
     u, tiny = torch.finfo(dt).eps / 2, torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
     Xd, E = X.double(), gate_up[0].shape[0]
@@ -104,7 +106,7 @@ def experts(X, ids, weights, gate_up, down, g):
         eg, eu = 2 * K * U32 * gua[:, :I], 2 * K * U32 * gua[:, I:]
         sl = gate * torch.special.expit(gate)
         h = sl * up
-        es = 1.1 * eg + 8 * 2 * U32 * sl.abs()
+        es = 1.1 * eg + (2 * gate.abs() + 8) * U32 * sl.abs()
         eh = es * up.abs() + (sl.abs() + es) * eu
         eh = eh + u * (h.abs() + eh) + tiny
         out = h @ Wd.T

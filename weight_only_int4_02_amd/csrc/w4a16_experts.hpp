@@ -1,0 +1,116 @@
+// Device helpers shared by the experts' kernels.
+#pragma once
+#include "w4a16_gemm_kernels.hpp"
+#include "w4a16_routed.hpp"
+
+namespace w4a16 {
+
+// v / (1 + exp(-v)).  exp2 and the reciprocal by the hardware's instructions,
+// each good to one step of 32 bits; the product v log2(e) before the exp2 is
+// rounded too, so the result is off by at most (2 |v| + 4) 2^-24 of itself --
+// nothing beside the rounding of h to 16 bits.  exp(-v) overflowing gives -0.
+__device__ __forceinline__ float silu(float v) {
+    return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * v));
+}
+
+template <bool BF>
+__device__ __forceinline__ void store_buffer16(__amdgpu_buffer_rsrc_t rsrc, uint32_t at, float v) {
+    if constexpr (BF)
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v), rsrc, (int)at, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (_Float16)v), rsrc, (int)at, 0, 0);
+}
+
+// bf16 weights by one fma each: (q - z) s = q s - z s, exact in fp32 (q s and z s
+// have at most 12 significant bits, the result 13), then one rounding to bf16.
+// Eight instructions of 31 less per word than dequant_word_bf16, which is what
+// the bf16 kernels are made of.  It gives +0 where that gives -0 (q = z, s < 0),
+// which no sum notices, and needs |s| < 2^124 (z s in range).
+struct Bf16Fma {
+    float s, nzs;   // s, -(z s)
+};
+__device__ __forceinline__ Bf16Fma bf16_fma(uint32_t sbits, uint32_t z) {
+    const float s = bf16_bits_to_float(sbits);
+    return {s, -((float)z * s)};
+}
+
+__device__ __forceinline__ bf8_t dequant_word_bf16_fma(uint32_t w, Bf16Fma g) {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+    const float q[8] = {(float)(lo & 0xFFu),         (float)((lo >> 16) & 0xFFu),
+                        (float)(hi & 0xFFu),         (float)((hi >> 16) & 0xFFu),
+                        (float)((lo >> 8) & 0xFFu),  (float)(lo >> 24),
+                        (float)((hi >> 8) & 0xFFu),  (float)(hi >> 24)};
+    u4_t o;
+#pragma unroll
+    for (int p = 0; p < 4; p++) {
+        const float a = __builtin_fmaf(q[2 * p], g.s, g.nzs), b = __builtin_fmaf(q[2 * p + 1], g.s, g.nzs);
+        asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(o[p]) : "v"(a), "v"(b));
+    }
+    return __builtin_bit_cast(bf8_t, o);
+}
+
+// mfma8_dequant_bf16 with that form: eight MFMAs with the next word's
+// dequantization between them, four vector instructions after each of the
+// first six, and the same FORMs and hazards.
+#define W4E_M(n) "v_mfma_f32_16x16x32_bf16 %[c" #n "], %[a" #n "], %[b], %[c" #n "]\n"
+#define W4E_BLOCK(P0, S0, P1, S1, P2, S2, P3, S3, P4, S4, P5, S5, P6, S6, P7, S7)                  \
+    asm volatile(P0 W4E_M(0) S0                                                                  \
+                 "v_and_b32 %[lo], %[m], %[w]\n"                                                 \
+                 "v_lshrrev_b32 %[hi], 4, %[w]\n"                                                \
+                 "v_and_b32 %[hi], %[m], %[hi]\n"                                                \
+                 "v_cvt_f32_ubyte0 %[f0], %[lo]\n" P1 W4E_M(1) S1                                \
+                 "v_cvt_f32_ubyte2 %[f1], %[lo]\n"                                               \
+                 "v_cvt_f32_ubyte0 %[f2], %[hi]\n"                                               \
+                 "v_cvt_f32_ubyte2 %[f3], %[hi]\n"                                               \
+                 "v_cvt_f32_ubyte1 %[f4], %[lo]\n" P2 W4E_M(2) S2                                \
+                 "v_cvt_f32_ubyte3 %[f5], %[lo]\n"                                               \
+                 "v_cvt_f32_ubyte1 %[f6], %[hi]\n"                                               \
+                 "v_cvt_f32_ubyte3 %[f7], %[hi]\n"                                               \
+                 "v_fma_f32 %[f0], %[f0], %[s], %[zs]\n" P3 W4E_M(3) S3                          \
+                 "v_fma_f32 %[f1], %[f1], %[s], %[zs]\n"                                         \
+                 "v_fma_f32 %[f2], %[f2], %[s], %[zs]\n"                                         \
+                 "v_fma_f32 %[f3], %[f3], %[s], %[zs]\n"                                         \
+                 "v_fma_f32 %[f4], %[f4], %[s], %[zs]\n" P4 W4E_M(4) S4                          \
+                 "v_fma_f32 %[f5], %[f5], %[s], %[zs]\n"                                         \
+                 "v_fma_f32 %[f6], %[f6], %[s], %[zs]\n"                                         \
+                 "v_fma_f32 %[f7], %[f7], %[s], %[zs]\n" P5 W4E_M(5) S5                          \
+                 "v_cvt_pk_bf16_f32 %[bn0], %[f0], %[f1]\n"                                      \
+                 "v_cvt_pk_bf16_f32 %[bn1], %[f2], %[f3]\n"                                      \
+                 "v_cvt_pk_bf16_f32 %[bn2], %[f4], %[f5]\n"                                      \
+                 "v_cvt_pk_bf16_f32 %[bn3], %[f6], %[f7]\n" P6 W4E_M(6) S6 P7 W4E_M(7) S7        \
+                 : [c0] "+v"(c0), [c1] "+v"(c1), [c2] "+v"(c2), [c3] "+v"(c3), [c4] "+v"(c4),    \
+                   [c5] "+v"(c5), [c6] "+v"(c6), [c7] "+v"(c7), [bn0] "=&v"(bn0),                \
+                   [bn1] "=&v"(bn1), [bn2] "=&v"(bn2), [bn3] "=&v"(bn3), [lo] "=&v"(lo),         \
+                   [hi] "=&v"(hi), [f0] "=&v"(f0), [f1] "=&v"(f1), [f2] "=&v"(f2),               \
+                   [f3] "=&v"(f3), [f4] "=&v"(f4), [f5] "=&v"(f5), [f6] "=&v"(f6),               \
+                   [f7] "=&v"(f7), [a0] "+v"(a[0]), [a1] "+v"(a[1]), [a2] "+v"(a[2]),            \
+                   [a3] "+v"(a[3]), [a4] "+v"(a[4]), [a5] "+v"(a[5]), [a6] "+v"(a[6]),           \
+                   [a7] "+v"(a[7])                                                               \
+                 : [b] "v"(b), [w] "v"(w), [zs] "v"(g.nzs), [s] "v"(g.s), [m] "s"(m),            \
+                   [ln] "v"(lds_next))
+#define W4E_PF(m, off) "ds_read_b128 %[a" #m "], %[ln] offset:" #off "\n"
+#define W4E_WT(n) "s_waitcnt lgkmcnt(" #n ")\n"
+template <int FORM>
+__device__ __forceinline__ h8_t mfma8_dequant_bf16_fma(f4_t &c0, f4_t &c1, f4_t &c2, f4_t &c3,
+                                                         f4_t &c4, f4_t &c5, f4_t &c6, f4_t &c7,
+                                                         h8_t (&a)[8], h8_t b, uint32_t w, Bf16Fma g,
+                                                         uint32_t m, uint32_t lds_next) {
+    uint32_t bn0, bn1, bn2, bn3, lo, hi;
+    float f0, f1, f2, f3, f4, f5, f6, f7;
+    if constexpr (FORM == 0)
+        W4E_BLOCK("", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
+    else if constexpr (FORM == 1)
+        W4E_BLOCK(W4E_WT(7), "", W4E_WT(6), "", W4E_WT(5), "", W4E_WT(4), "", W4E_WT(3), "",
+                  W4E_WT(2), "", W4E_WT(1), "", W4E_WT(0), "");
+    else
+        W4E_BLOCK("", W4E_PF(0, 0), "", W4E_PF(1, 4096), "", W4E_PF(2, 8192), "",
+                  W4E_PF(3, 12288), "", W4E_PF(4, 16384), "", W4E_PF(5, 20480), "",
+                  W4E_PF(6, 24576), "", W4E_PF(7, 28672));
+    return __builtin_bit_cast(h8_t, u4_t{bn0, bn1, bn2, bn3});
+}
+#undef W4E_PF
+#undef W4E_WT
+#undef W4E_BLOCK
+#undef W4E_M
+
+}  // namespace w4a16

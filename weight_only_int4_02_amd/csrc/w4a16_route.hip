@@ -233,7 +233,8 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
                                                                    int tiles_max,
                                                                    ExpertTile *__restrict__ tiles,
                                                                    int32_t *__restrict__ tiles_used,
-                                                                   int32_t *__restrict__ perm) {
+                                                                   int32_t *__restrict__ perm,
+                                                                   int32_t *__restrict__ place) {
     __shared__ int count[kMaxExperts];
     __shared__ int part[kPlanThreads / 64][3];
     __shared__ int wave_n[kPlanThreads / 64];
@@ -295,8 +296,11 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
             before += w < wave ? wave_n[w] : 0;
             n += wave_n[w];
         }
-        if (hit)
-            perm[at + before + __popcll(b & ((1ull << lane) - 1))] = i;
+        if (hit) {
+            const int p = at + before + __popcll(b & ((1ull << lane) - 1));
+            perm[p] = i;
+            place[i] = p;
+        }
         at += n;
         __syncthreads();
     }
@@ -304,7 +308,7 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
 
 // ---------------------------------------------------------------------------
 // Y[t] = RNE(sum over the slots with an expert of weights[t][j] P[t][j]), in
-// slot order; P rows of other slots hold nothing and are not read.  Four
+// slot order; slots without an expert have no row of P.  Four
 // columns per thread where D is a multiple of 4.
 // ---------------------------------------------------------------------------
 template <bool BF, int C>
@@ -322,7 +326,8 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
             if (id < 0 || id >= a.E)
                 continue;
             const float w = a.weights[t * a.k + j];
-            const float *p = a.P + (t * a.k + j) * a.D + d;
+            const int64_t row = a.place ? a.place[t * a.k + j] : t * a.k + j;
+            const float *p = a.P + row * a.D + d;
             if constexpr (C == 4) {
                 const f4_t v = *(const f4_t *)p;
 #pragma unroll
@@ -372,9 +377,9 @@ int launch_route(const RouteArgs &a, int logits_dtype, void *stream) {
 }
 
 int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
-                       int32_t *tiles_used, int32_t *perm, void *stream) {
+                       int32_t *tiles_used, int32_t *perm, int32_t *place, void *stream) {
     hipLaunchKernelGGL(expert_plan_kernel, dim3((unsigned)E), dim3(kPlanThreads), 0,
-                       (hipStream_t)stream, ids, R, E, bm, tiles_max, tiles, tiles_used, perm);
+                       (hipStream_t)stream, ids, R, E, bm, tiles_max, tiles, tiles_used, perm, place);
     return (int)hipGetLastError();
 }
 

@@ -42,7 +42,7 @@ struct ExpertsPlan {
     int mt;              // small kernel: 16-row activation tiles per workgroup
     int bm;              // rows per tile
     int64_t tiles;       // tiles launched (an upper bound)
-    size_t used_off, tiles_off, perm_off, h_off, p_off, ws_bytes;
+    size_t used_off, tiles_off, perm_off, place_off, h_off, p_off, ws_bytes;
 };
 ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int64_t E, int32_t g,
                          uint32_t flags);
@@ -52,7 +52,8 @@ ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int6
 struct ExpertsArgs {
     const uint16_t *X;      // 16-bit rows of K
     const void *qd, *sd, *zd;
-    void *Y;                // gated: h, 16-bit [rows][N]; else fp32 [T k][N]
+    void *Y;                // gated: h, 16-bit [T k][N]; else P, fp32 [T k][N]; rows in the
+                            // plan's order (direct: by their flat numbers)
     const int32_t *ids;     // [R]
     const int32_t *perm;    // sorted position -> flat row (plan)
     const ExpertTile *tiles;  // (plan)
@@ -65,6 +66,7 @@ struct ExpertsArgs {
 struct CombineArgs {
     const float *P;         // [T k][D]
     const int32_t *ids;
+    const int32_t *place;   // flat row -> its row of P (plan), or null: the same
     const float *weights;
     uint16_t *Y;            // [T][D]
     int64_t T, D;
@@ -72,7 +74,7 @@ struct CombineArgs {
 };
 
 int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
-                       int32_t *tiles_used, int32_t *perm, void *stream);
+                       int32_t *tiles_used, int32_t *perm, int32_t *place, void *stream);
 int launch_experts_small(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_small_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_large(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);

@@ -83,13 +83,14 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
     ExpertTile *tiles = (ExpertTile *)(ws + p.tiles_off);
     int32_t *used = (int32_t *)(ws + p.used_off);
     int32_t *perm = (int32_t *)(ws + p.perm_off);
+    int32_t *place = (int32_t *)(ws + p.place_off);
     uint16_t *h = (uint16_t *)(ws + p.h_off);
     float *P = (float *)(ws + p.p_off);
     const int R = (int)(T * k);
     const bool bf = (flags & W4A16_BF16) != 0;
     int e = 0;
     if (!p.direct)
-        e = launch_expert_plan(ids, R, (int)E, p.bm, (int)p.tiles, tiles, used, perm, stream);
+        e = launch_expert_plan(ids, R, (int)E, p.bm, (int)p.tiles, tiles, used, perm, place, stream);
     ExpertsArgs gu = product(X, T, K, gate_up_q, gate_up_s, gate_up_z, I, g, flags);
     ExpertsArgs dn = product(h, R, I, down_q, down_s, down_z, D, g, flags);
     gu.Y = h;
@@ -115,6 +116,7 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
         c.P = P;
         c.ids = ids;
         c.weights = weights;
+        c.place = p.direct ? nullptr : place;
         c.Y = Y;
         c.T = T;
         c.D = D;

@@ -41,8 +41,8 @@ int32_t check_experts_shape(int64_t T, int32_t k, int64_t K, int64_t I, int64_t 
     if (2 * gu.NT * gu.KT * 1024 >= (int64_t(1) << 31) ||
         dn.NT * dn.KT * 1024 >= (int64_t(1) << 31) || T * K * 2 >= (int64_t(1) << 31))
         return W4A16_ERR_SHAPE;
-    // a tile's h rows too
-    if (128 * I * 2 >= (int64_t(1) << 31))
+    // a tile's rows of h and P too
+    if (128 * I * 2 >= (int64_t(1) << 31) || 128 * D * 4 >= (int64_t(1) << 31))
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
@@ -82,6 +82,8 @@ ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int6
     p.tiles_off = at;
     at += p.direct ? 0 : up256((size_t)p.tiles * sizeof(ExpertTile));
     p.perm_off = at;
+    at += p.direct ? 0 : up256((size_t)R * 4);
+    p.place_off = at;
     at += p.direct ? 0 : up256((size_t)R * 4);
     p.h_off = at;
     at += up256((size_t)R * (size_t)I * 2);
