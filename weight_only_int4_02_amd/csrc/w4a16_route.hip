@@ -223,30 +223,49 @@ void launch_route_wide(const RouteArgs &a, int dt, bool wide, unsigned blocks, h
 // ---------------------------------------------------------------------------
 // The plan: rows sorted by expert, in their own order within an expert, and
 // the list of tiles.  One workgroup per expert, each with its own count of
-// all experts (integer adds in LDS: their order changes nothing), then its
-// own rows written in order.  No workgroup waits for another.
+// all experts (integer adds in LDS: their order changes nothing).  Each wave
+// takes a run of rows, counts its expert's in it, and after the one barrier
+// that shares the counts writes their places in order; no workgroup waits for
+// another.  (With a barrier for every 1024 rows: 32 us for 24576 rows.)
 // ---------------------------------------------------------------------------
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kPlanWaves = kPlanThreads / 64;
 
-__global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t *__restrict__ ids,
-                                                                   int R, int E, int bm,
-                                                                   int tiles_max,
-                                                                   ExpertTile *__restrict__ tiles,
-                                                                   int32_t *__restrict__ tiles_used,
-                                                                   int32_t *__restrict__ perm,
-                                                                   int32_t *__restrict__ place) {
+__global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(
+    const int32_t *__restrict__ ids, int R, int E, int bm, int tiles_max,
+    ExpertTile *__restrict__ tiles, int32_t *__restrict__ tiles_used, int32_t *__restrict__ perm,
+    int32_t *__restrict__ place) {
     __shared__ int count[kMaxExperts];
-    __shared__ int part[kPlanThreads / 64][3];
-    __shared__ int wave_n[kPlanThreads / 64];
+    __shared__ int part[kPlanWaves][3];
+    __shared__ int wave_n[kPlanWaves];
     const int e = blockIdx.x, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    count[tid] = 0;
     static_assert(kPlanThreads == kMaxExperts, "one thread per expert");
+    count[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < R; i += kPlanThreads) {
-        const int id = ids[i];
+    // the wave's rows: blocks of 64, eight of them loaded at once
+    constexpr int U = 8;
+    const int blocks = (R + 63) / 64, per = (blocks + kPlanWaves - 1) / kPlanWaves;
+    const int b0 = min(blocks, wave * per), b1 = min(blocks, b0 + per);
+    auto each_block = [&](auto &&f) __attribute__((always_inline)) {
+        for (int b = b0; b < b1; b += U) {
+            int id[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const int i = (b + u) * 64 + lane;
+                id[u] = b + u < b1 && i < R ? ids[i] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++)
+                f(id[u], (b + u) * 64 + lane);
+        }
+    };
+    int hits = 0;
+    each_block([&](int id, int) {
         if (id >= 0 && id < E)
             atomicAdd(&count[id], 1);
-    }
+        hits += __popcll(__ballot(id == e));
+    });
+    if (lane == 0)
+        wave_n[wave] = hits;
     __syncthreads();
     // rows and tiles of the experts before this one, and tiles of all
     {
@@ -264,11 +283,12 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
         }
     }
     __syncthreads();
-    int row0 = 0, tile0 = 0, used = 0;
-    for (int w = 0; w < kPlanThreads / 64; w++) {
+    int row0 = 0, tile0 = 0, used = 0, at = 0;
+    for (int w = 0; w < kPlanWaves; w++) {
         row0 += part[w][0];
         tile0 += part[w][1];
         used += part[w][2];
+        at += w < wave ? wave_n[w] : 0;
     }
     const int mine = count[e];
     for (int i = tid; i * bm < mine; i += kPlanThreads)
@@ -281,29 +301,18 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
         if (tid == 0)
             *tiles_used = used;
     }
-    if (mine == 0)
+    if (hits == 0)
         return;
-    int at = row0;
-    for (int i0 = 0; i0 < R; i0 += kPlanThreads) {
-        const int i = i0 + tid;
-        const bool hit = i < R && ids[i] == e;
-        const uint64_t b = __ballot(hit);
-        if (lane == 0)
-            wave_n[wave] = __popcll(b);
-        __syncthreads();
-        int before = 0, n = 0;
-        for (int w = 0; w < kPlanThreads / 64; w++) {
-            before += w < wave ? wave_n[w] : 0;
-            n += wave_n[w];
-        }
-        if (hit) {
-            const int p = at + before + __popcll(b & ((1ull << lane) - 1));
+    at += row0;
+    each_block([&](int id, int i) {
+        const uint64_t b = __ballot(id == e);
+        if (id == e) {
+            const int p = at + __popcll(b & ((1ull << lane) - 1));
             perm[p] = i;
             place[i] = p;
         }
-        at += n;
-        __syncthreads();
-    }
+        at += __popcll(b);
+    });
 }
 
 // ---------------------------------------------------------------------------
@@ -311,50 +320,76 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(const int32_t
 // slot order; slots without an expert have no row of P.  Four
 // columns per thread where D is a multiple of 4.
 // ---------------------------------------------------------------------------
+// Columns are cut into blocks of 256 C; a workgroup takes one block of a row.
 template <bool BF, int C>
 __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
-    const int64_t per_row = a.D / C, n = a.T * per_row;
-    const int64_t stride = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
-        const int64_t t = i / per_row, d = (i - t * per_row) * C;
+    const int64_t d = ((int64_t)blockIdx.x * 256 + threadIdx.x) * C;
+    if (d >= a.D)
+        return;
+    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
         float acc[C];
 #pragma unroll
         for (int c = 0; c < C; c++)
             acc[c] = 0.f;
-        for (int j = 0; j < a.k; j++) {
-            const int id = a.ids[t * a.k + j];
-            if (id < 0 || id >= a.E)
-                continue;
-            const float w = a.weights[t * a.k + j];
-            const int64_t row = a.place ? a.place[t * a.k + j] : t * a.k + j;
-            const float *p = a.P + row * a.D + d;
-            if constexpr (C == 4) {
-                const f4_t v = *(const f4_t *)p;
+        // (the slots' numbers are the same for the whole workgroup)
+        constexpr int U = 4;   // slots whose loads are in flight together
+        for (int j0 = 0; j0 < a.k; j0 += U) {
+            float w[U], v[U][C];
+            bool in[U];
 #pragma unroll
-                for (int c = 0; c < 4; c++)
-                    acc[c] += w * v[c];
-            } else {
-                acc[0] += w * p[0];
+            for (int u = 0; u < U; u++) {
+                const int64_t s = t * a.k + j0 + u;
+                in[u] = j0 + u < a.k;
+                const int id = in[u] ? a.ids[s] : -1;
+                in[u] = id >= 0 && id < a.E;
+                if (in[u]) {
+                    w[u] = a.weights[s];
+                    const float *p = a.P + (a.place ? (int64_t)a.place[s] : s) * a.D + d;
+                    if constexpr (C == 4) {
+                        const f4_t x = *(const f4_t *)p;
+#pragma unroll
+                        for (int c = 0; c < C; c++)
+                            v[u][c] = x[c];
+                    } else {
+                        v[u][0] = *p;
+                    }
+                }
             }
-        }
 #pragma unroll
-        for (int c = 0; c < C; c++)
-            store_out16<BF>(a.Y + t * a.D + d + c, acc[c]);
+            for (int u = 0; u < U; u++)
+                if (in[u]) {
+#pragma unroll
+                    for (int c = 0; c < C; c++)
+                        acc[c] += w[u] * v[u][c];
+                }
+        }
+        uint16_t out[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if constexpr (BF)
+                out[c] = __builtin_bit_cast(uint16_t, (__bf16)acc[c]);
+            else
+                out[c] = __builtin_bit_cast(uint16_t, (_Float16)acc[c]);
+        }
+        uint16_t *y = a.Y + t * a.D + d;
+        if constexpr (C == 4) {
+            typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+            *(u2_t *)y = u2_t{out[0] | (uint32_t)out[1] << 16, out[2] | (uint32_t)out[3] << 16};
+        } else {
+            y[0] = out[0];
+        }
     }
 }
 
 template <bool BF>
 void launch_combine(const CombineArgs &a, hipStream_t st) {
     const int c = (a.D & 3) == 0 ? 4 : 1;
-    int64_t blocks = (a.T * (a.D / c) + 255) / 256;
-    if (blocks > 16384)
-        blocks = 16384;
+    const dim3 grid((unsigned)((a.D + 256 * c - 1) / (256 * c)),
+                    (unsigned)(a.T < 32768 ? a.T : 32768));
     if (c == 4)
-        hipLaunchKernelGGL((experts_combine_kernel<BF, 4>), dim3((unsigned)blocks), dim3(256), 0,
-                           st, a);
+        hipLaunchKernelGGL((experts_combine_kernel<BF, 4>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL((experts_combine_kernel<BF, 1>), dim3((unsigned)blocks), dim3(256), 0,
-                           st, a);
+        hipLaunchKernelGGL((experts_combine_kernel<BF, 1>), grid, dim3(256), 0, st, a);
 }
 
 }  // namespace
