@@ -14,7 +14,8 @@ namespace w4a16 {
 namespace {
 
 // ---------------------------------------------------------------------------
-// w4a16_route: one wave per row; lane l holds experts l, l + 64, ...
+// w4a16_route.  A row takes L = 16 lanes (up to 256 experts) or a whole wave;
+// lane l holds the V experts from l V on.
 //
 // Which expert is larger must not hang on the rounding of an exponential:
 // without a bias, and with groups judged by their best expert alone, the
@@ -22,10 +23,14 @@ namespace {
 // rise), and the keys are the logits themselves.  Otherwise (WIDE) scores and
 // keys are formed in 64 bits.
 //
-// The k largest are taken one at a time: a wave-wide maximum of the keys (DPP
-// moves, no LDS), then the first lane and slot that holds it -- expert l + 64
-// v, so the lowest slot with a holder, and in it the lowest lane, is the
-// lowest index.  A taken or excluded expert's key is -infinity.
+// The k largest are taken one at a time: the maximum over the row's lanes by
+// DPP moves, then the lowest expert that holds it.  A taken or excluded
+// expert's key is -infinity.  The chosen experts' scores are formed anew from
+// their logits at the end, one lane a slot.
+//
+// The kernel is bound by its instructions, not its bytes (8192 rows of 256
+// experts: 9 MB): with a wave to each row the reductions, the same for all of
+// a row's lanes, took 23 us; four rows to a wave share them.
 // ---------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
@@ -42,22 +47,18 @@ __device__ __forceinline__ double dpp(double v) {
     const uint32_t hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(b >> 32));
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ float lane_value(float v, int l) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), l));
-}
-__device__ __forceinline__ double lane_value(double v, int l) {
-    const uint64_t b = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, l);
-    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), l);
-    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
-}
-template <typename T, typename F>
-__device__ __forceinline__ T wave_reduce(T v, F op) {
+// op over the L lanes of a row; every lane gets the result.
+template <int L, typename T, typename F>
+__device__ __forceinline__ T row_reduce(T v, F op) {
     v = op(v, dpp<0xB1>(v));   // lanes 1 apart
     v = op(v, dpp<0x4E>(v));   // 2 apart
     v = op(v, dpp<0x141>(v));  // mirrored within 8
-    v = op(v, dpp<0x140>(v));  // mirrored within 16: every lane has its 16's
-    return op(op(lane_value(v, 0), lane_value(v, 16)), op(lane_value(v, 32), lane_value(v, 48)));
+    v = op(v, dpp<0x140>(v));  // mirrored within 16
+    if constexpr (L == 64) {
+        v = op(v, __shfl_xor(v, 16));
+        v = op(v, __shfl_xor(v, 32));
+    }
+    return v;
 }
 __device__ __forceinline__ float vmax(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double vmax(double a, double b) { return fmax(a, b); }
@@ -71,153 +72,275 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t at) {
     else
         return (float)((const _Float16 *)p)[at];
 }
+__device__ __forceinline__ float clean_logit(float x) {
+    return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
+}
 
-constexpr int kRouteWaves = 4;
+// exp(x) in 64 bits, without the branches of a library's: x = n ln 2 + r with
+// |r| <= ln 2 / 2 (ln 2 in two parts, so that n times the first is exact), the
+// exponential's series to r^13 / 13! (the next term is below 2^-57), times
+// 2^n.  Below -745 it is 0, above 709 infinite, as the rounded exponential is.
+__device__ __forceinline__ double exp_series(double arg) {
+    const double x = fmin(fmax(arg, -745.0), 709.0);
+    const double n = __builtin_rint(x * 1.4426950408889634);
+    const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
+    double y = 1.0 / 6227020800.0;
+    constexpr double over[13] = {1.0 / 479001600.0, 1.0 / 39916800.0, 1.0 / 3628800.0, 1.0 / 362880.0,
+                                 1.0 / 40320.0,     1.0 / 5040.0,     1.0 / 720.0,     1.0 / 120.0,
+                                 1.0 / 24.0,        1.0 / 6.0,        0.5,             1.0,
+                                 1.0};
+#pragma unroll
+    for (int k = 0; k < 13; k++)
+        y = fma(y, r, over[k]);
+    y = ldexp(y, (int)n);
+    return arg < -745.0 ? 0.0 : arg > 709.0 ? (double)INFINITY : y;
+}
+// 1 / v for 1 <= v (0 above 1e300), by two steps of Newton's from the
+// hardware's estimate.
+__device__ __forceinline__ double reciprocal(double v) {
+    double y = __builtin_amdgcn_rcp(v);
+    y = fma(y, fma(-v, y, 1.0), y);
+    y = fma(y, fma(-v, y, 1.0), y);
+    return v > 1e300 ? 0.0 : y;
+}
 
-template <int V, bool WIDE, int DT>
-__global__ __launch_bounds__(kRouteWaves * 64) void route_kernel(RouteArgs a) {
+// A logit's score: sigmoid, or softmax's numerator.  -infinity has none.
+template <typename Key>
+__device__ __forceinline__ Key score_of(float l, float top, bool sigmoid) {
+    Key s;
+    if constexpr (sizeof(Key) == 8) {
+        const double e = exp_series(sigmoid ? -(double)l : (double)l - (double)top);
+        s = sigmoid ? reciprocal(1.0 + e) : e;
+    } else {
+        const float e = expf(sigmoid ? -l : l - top);
+        s = sigmoid ? 1.f / (1.f + e) : e;
+    }
+    return l == -INFINITY ? 0 : s;
+}
+
+constexpr int kRouteThreads = 256;
+
+template <int V, int L, bool WIDE, int DT>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     using Key = std::conditional_t<WIDE, double, float>;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int t = (int)blockIdx.x * kRouteWaves + wave;
-    if (t >= a.T)
-        return;
+    constexpr int ROWS = kRouteThreads / L;
+    constexpr int NQ = 64 / L;       // groups of experts per lane, at most
+    constexpr int none_index = 1 << 30;
+    const int l = threadIdx.x % L, row = threadIdx.x / L;
+    // (rows past the last repeat it, and store nothing: every lane stays
+    // active for the moves between lanes)
+    const int64_t t_own = (int64_t)blockIdx.x * ROWS + row;
+    const int64_t t = t_own < a.T ? t_own : a.T - 1;
+    const int64_t base = t * a.E;
     const Key none = -(Key)INFINITY;
-    float l[V];
-    float top = -INFINITY;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        const int e = lane + 64 * v;
-        const float x = e < a.E ? load_logit<DT>(a.logits, (int64_t)t * a.E + e) : -INFINITY;
-        l[v] = x != x ? -INFINITY : fminf(x, 3.402823466e38f);
-        top = fmaxf(top, l[v]);
-    }
-    top = wave_reduce(top, [](float x, float y) { return fmaxf(x, y); });
-    // scores: softmax's numerator, or sigmoid; a row with nothing has none
     const bool sig = a.sigmoid != 0;
-    Key s[V], key[V];
-    Key sum = 0;
-#pragma unroll
-    for (int v = 0; v < V; v++) {
-        if constexpr (WIDE) {
-            s[v] = l[v] == -INFINITY ? 0.0
-                   : sig             ? 1.0 / (1.0 + exp(-(double)l[v]))
-                                     : exp((double)l[v] - (double)top);
-        } else {
-            s[v] = l[v] == -INFINITY ? 0.f : sig ? 1.f / (1.f + expf(-l[v])) : expf(l[v] - top);
-        }
-        sum += s[v];
-    }
-    if (!sig) {
-        sum = wave_reduce(sum, [](Key x, Key y) { return x + y; });
-        const Key inv = sum > 0 ? 1 / sum : 0;
+    const auto larger = [](auto x, auto y) { return vmax(x, y); };
+    float lg[V];
+    float top = -INFINITY;
+    const int own = a.E - l * V;      // the lane's experts that there are
+    if (a.E == V * L) {
 #pragma unroll
         for (int v = 0; v < V; v++)
-            s[v] *= inv;
+            lg[v] = load_logit<DT>(a.logits, base + l * V + v);
+    } else {
+        // (past the row's end, its last logit is loaded and dropped)
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            const float x = load_logit<DT>(a.logits, base + min(l * V + v, a.E - 1));
+            lg[v] = v < own ? x : -INFINITY;
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; v++) {
+        lg[v] = clean_logit(lg[v]);
+        top = fmaxf(top, lg[v]);
+    }
+    // softmax's denominator, and the keys
+    Key key[V], inv = 1;
+    if (!sig || WIDE) {
+        if (!sig)
+            top = row_reduce<L>(top, larger);
+        Key sum = 0;
+#pragma unroll
+        for (int v = 0; v < V; v++) {
+            key[v] = score_of<Key>(lg[v], top, sig);
+            sum += key[v];
+        }
+        if (!sig) {
+            sum = row_reduce<L>(sum, [](Key x, Key y) { return x + y; });
+            inv = sum > 0 ? 1 / sum : 0;
+        }
     }
 #pragma unroll
     for (int v = 0; v < V; v++) {
         if constexpr (WIDE) {
-            const int e = lane + 64 * v;
-            key[v] = s[v];
-            if (a.bias && e < a.E) {
-                key[v] += (double)a.bias[e];
+            key[v] *= inv;
+            if (a.bias) {
+                key[v] += (double)a.bias[min(l * V + v, a.E - 1)];
                 key[v] = key[v] != key[v] ? none : key[v];
             }
-            if (l[v] == -INFINITY)
-                key[v] = none;
+            key[v] = lg[v] == -INFINITY ? none : key[v];
         } else {
-            key[v] = l[v];
+            key[v] = lg[v];
         }
     }
 
     if (a.topk_groups < a.n_groups) {
-        // the keys go through LDS, so that lane q can walk group q; only this
-        // wave reads what it wrote
-        __shared__ Key ks[kRouteWaves][V * 64];
-#pragma unroll
-        for (int v = 0; v < V; v++)
-            ks[wave][lane + 64 * v] = key[v];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         const int size = a.E / a.n_groups;
-        Key best = none, second = none;
-        if (lane < a.n_groups) {
-            for (int i = 0; i < size; i++) {
-                const Key x = ks[wave][lane * size + i];
-                second = vmax(second, x < best ? x : best);
-                best = vmax(best, x);
+        // the two best keys of each group; value[q] of lane l: group l + q L
+        Key value[NQ];
+        const auto take = [&](Key &best, Key &second, Key x) {
+            second = vmax(second, x < best ? x : best);
+            best = vmax(best, x);
+        };
+        __shared__ Key ks[ROWS][V * L + V * L / 16];
+        if (L == 16 && size == 2 * V) {
+            // a group is two lanes' keys: they meet by one move, and lane q
+            // fetches group q's value
+            Key best = none, second = none;
+#pragma unroll
+            for (int v = 0; v < V; v++)
+                take(best, second, key[v]);
+            const Key b2 = dpp<0xB1>(best), s2 = dpp<0xB1>(second);
+            take(best, second, b2);
+            take(best, second, s2);
+            const Key x = a.group_top == 2 && second != none ? best + second : best;
+            const Key y = __shfl(x, (int)(threadIdx.x & 48) + ((2 * l) & 15));
+            value[0] = l < a.n_groups ? y : none;
+#pragma unroll
+            for (int q = 1; q < NQ; q++)
+                value[q] = none;
+        } else {
+            // the keys go through LDS, so that lane q can walk groups q, q +
+            // L, ...; a row's lanes are one wave's, so no barrier.  One place
+            // in 17 is left out, or the walks of groups of 32 would meet in
+            // one bank.
+#pragma unroll
+            for (int v = 0; v < V; v++) {
+                const int e = l * V + v;
+                ks[row][e + e / 16] = key[v];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+            for (int q = 0; q < NQ; q++) {
+                Key best = none, second = none;
+                const int grp = l + q * L;
+                const int n = grp < a.n_groups ? size : 0;
+                for (int i0 = 0; i0 < n; i0 += 8) {
+                    Key x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int e = grp * size + min(i0 + i, size - 1);
+                        x[i] = ks[row][e + e / 16];
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        take(best, second, i0 + i < size ? x[i] : none);
+                }
+                value[q] = a.group_top == 2 && second != none ? best + second : best;
             }
         }
-        Key value = best;
-        if (a.group_top == 2 && second != none)
-            value += second;
         uint64_t keep = 0;
         for (int i = 0; i < a.topk_groups; i++) {
-            const Key m = wave_reduce(value, [](Key x, Key y) { return vmax(x, y); });
-            const uint64_t at = __ballot(value == m && lane < a.n_groups && !(keep >> lane & 1));
-            const int q = __builtin_ctzll(at);
-            keep |= 1ull << q;
-            value = lane == q ? none : value;
+            Key m = value[0];
+#pragma unroll
+            for (int q = 1; q < NQ; q++)
+                m = vmax(m, value[q]);
+            m = row_reduce<L>(m, larger);
+            int at = none_index;
+#pragma unroll
+            for (int q = NQ - 1; q >= 0; q--) {
+                const int grp = l + q * L;
+                at = value[q] == m && grp < a.n_groups && !(keep >> grp & 1) ? grp : at;
+            }
+            at = row_reduce<L>(at, [](int x, int y) { return x < y ? x : y; });
+            keep |= 1ull << (at & 63);
+#pragma unroll
+            for (int q = 0; q < NQ; q++)
+                value[q] = l + q * L == at ? none : value[q];
         }
+        int grp = l * V / size, rest = l * V - grp * size;   // of the lane's experts
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            const int q = (lane + 64 * v) / size;
-            if (q >= 64 || !(keep >> q & 1))
+            if (grp >= a.n_groups || !(keep >> grp & 1))
                 key[v] = none;
+            if (++rest == size) {
+                rest = 0;
+                grp++;
+            }
         }
     }
 
-    int id = -1;      // lane j: slot j
-    Key weight = 0, total = 0;
+    // slots l and l + L (k is at most 32)
+    constexpr int NS = L == 16 ? 2 : 1;
+    int id[NS];
+#pragma unroll
+    for (int n = 0; n < NS; n++)
+        id[n] = -1;
     for (int j = 0; j < a.k; j++) {
         Key m = key[0];
 #pragma unroll
         for (int v = 1; v < V; v++)
             m = vmax(m, key[v]);
-        m = wave_reduce(m, [](Key x, Key y) { return vmax(x, y); });
-        if (m == none)
-            break;
-        bool found = false;
+        m = row_reduce<L>(m, larger);
+        int at = none_index;
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            const uint64_t at = __ballot(key[v] == m);
-            if (!found && at) {
-                found = true;
-                const int q = __builtin_ctzll(at);
-                const Key w = lane_value(s[v], q);
-                total += w;
-                if (lane == j) {
-                    id = q + 64 * v;
-                    weight = w;
-                }
-                key[v] = lane == q ? none : key[v];
-            }
+        for (int v = V - 1; v >= 0; v--)
+            at = key[v] == m ? v : at;
+        at += l * V;
+        at = row_reduce<L>(at, [](int x, int y) { return x < y ? x : y; });
+        at = m == none ? -1 : at;
+        const int mine = at - l * V;
+#pragma unroll
+        for (int v = 0; v < V; v++)
+            key[v] = v == mine ? none : key[v];
+#pragma unroll
+        for (int n = 0; n < NS; n++)
+            id[n] = j == l + n * L ? at : id[n];
+    }
+
+    Key w[NS], total = 0;
+#pragma unroll
+    for (int n = 0; n < NS; n++) {
+        const float x =
+            id[n] < 0 ? -INFINITY : clean_logit(load_logit<DT>(a.logits, base + id[n]));
+        w[n] = score_of<Key>(x, top, sig) * inv;
+        total += w[n];
+    }
+    if (a.renormalize) {
+        total = row_reduce<L>(total, [](Key x, Key y) { return x + y; });
+#pragma unroll
+        for (int n = 0; n < NS; n++)
+            w[n] = total > 0 ? w[n] / total : 0;
+    }
+#pragma unroll
+    for (int n = 0; n < NS; n++) {
+        const int j = l + n * L;
+        if (t_own < a.T && j < a.k) {
+            a.ids[t * a.k + j] = id[n];
+            a.weights[t * a.k + j] = id[n] < 0 ? 0.f : (float)(w[n] * (Key)a.scale);
         }
     }
-    if (lane < a.k) {
-        if (a.renormalize)
-            weight = total > 0 ? weight / total : 0;
-        a.ids[(int64_t)t * a.k + lane] = id;
-        a.weights[(int64_t)t * a.k + lane] = id < 0 ? 0.f : (float)(weight * (Key)a.scale);
-    }
 }
 
-template <int V, bool WIDE>
-void launch_route_typed(const RouteArgs &a, int dt, unsigned blocks, hipStream_t st) {
-    const dim3 grid(blocks), block(kRouteWaves * 64);
+template <int V, int L, bool WIDE>
+void launch_route_typed(const RouteArgs &a, int dt, hipStream_t st) {
+    constexpr int ROWS = kRouteThreads / L;
+    const dim3 grid((unsigned)((a.T + ROWS - 1) / ROWS)), block(kRouteThreads);
     if (dt == W4A16_LOGITS_F32)
-        hipLaunchKernelGGL((route_kernel<V, WIDE, W4A16_LOGITS_F32>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_F32>), grid, block, 0, st, a);
     else if (dt == W4A16_LOGITS_BF16)
-        hipLaunchKernelGGL((route_kernel<V, WIDE, W4A16_LOGITS_BF16>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_BF16>), grid, block, 0, st, a);
     else
-        hipLaunchKernelGGL((route_kernel<V, WIDE, W4A16_LOGITS_F16>), grid, block, 0, st, a);
+        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_F16>), grid, block, 0, st, a);
 }
 
-template <int V>
-void launch_route_wide(const RouteArgs &a, int dt, bool wide, unsigned blocks, hipStream_t st) {
+template <int V, int L>
+void launch_route_wide(const RouteArgs &a, int dt, bool wide, hipStream_t st) {
     if (wide)
-        launch_route_typed<V, true>(a, dt, blocks, st);
+        launch_route_typed<V, L, true>(a, dt, st);
     else
-        launch_route_typed<V, false>(a, dt, blocks, st);
+        launch_route_typed<V, L, false>(a, dt, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -396,18 +519,19 @@ void launch_combine(const CombineArgs &a, hipStream_t st) {
 
 int launch_route(const RouteArgs &a, int logits_dtype, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
-    const unsigned blocks = (unsigned)((a.T + kRouteWaves - 1) / kRouteWaves);
     const bool wide = a.bias != nullptr || (a.topk_groups < a.n_groups && a.group_top == 2);
-    if (a.E <= 64)
-        launch_route_wide<1>(a, logits_dtype, wide, blocks, st);
+    if (a.E <= 16)
+        launch_route_wide<1, 16>(a, logits_dtype, wide, st);
+    else if (a.E <= 64)
+        launch_route_wide<4, 16>(a, logits_dtype, wide, st);
     else if (a.E <= 128)
-        launch_route_wide<2>(a, logits_dtype, wide, blocks, st);
+        launch_route_wide<8, 16>(a, logits_dtype, wide, st);
     else if (a.E <= 256)
-        launch_route_wide<4>(a, logits_dtype, wide, blocks, st);
+        launch_route_wide<16, 16>(a, logits_dtype, wide, st);
     else if (a.E <= 512)
-        launch_route_wide<8>(a, logits_dtype, wide, blocks, st);
+        launch_route_wide<8, 64>(a, logits_dtype, wide, st);
     else
-        launch_route_wide<16>(a, logits_dtype, wide, blocks, st);
+        launch_route_wide<16, 64>(a, logits_dtype, wide, st);
     return (int)hipGetLastError();
 }
 
