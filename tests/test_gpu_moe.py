@@ -29,7 +29,10 @@ def check_route(logits, k, **kw):
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 2), (3, 5, 5), (7, 64, 6), (4, 65, 8), (130, 128, 8),
-                                   (33, 256, 32), (5, 511, 7), (2, 1024, 16), (2001, 160, 6)])
+                                   (33, 256, 32), (5, 511, 7), (2, 1024, 16), (2001, 160, 6),
+                                   # many rows: several to a wave
+                                   (2049, 8, 2), (2065, 16, 16), (2050, 31, 20), (2100, 64, 8),
+                                   (2051, 100, 32), (2500, 250, 8), (2052, 256, 8), (2053, 300, 3)])
 def test_route_plain(T, E, k, dt):
     l = torch.randn((T, E), generator=gen(T + E)).mul(2).to(DT[dt])
     for score in ("softmax", "sigmoid"):
@@ -41,14 +44,17 @@ def test_route_plain(T, E, k, dt):
 @pytest.mark.parametrize("group_top", [1, 2])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("E,groups,topk,k", [(8, 2, 1, 4), (64, 64, 5, 5), (160, 8, 3, 6), (256, 8, 4, 8), (60, 4, 4, 9)])
-def test_route_groups_and_bias(E, groups, topk, k, biased, group_top, score):
-    l = torch.randn((65, E), generator=gen(E))
+@pytest.mark.parametrize("T", [65, 2061])
+def test_route_groups_and_bias(T, E, groups, topk, k, biased, group_top, score):
+    l = torch.randn((T, E), generator=gen(E))
     bias = torch.randn(E, generator=gen(E + 1)).mul(0.1) if biased else None
     check_route(l, k, score=score, bias=bias, groups=groups, topk_groups=topk, group_top=group_top)
 
 
 def test_route_ties_go_to_the_lowest_index():
-    l = torch.randint(-2, 3, (300, 96), generator=gen(3)).float()
+    l = torch.randint(-2, 3, (2300, 96), generator=gen(3)).float()
+    for rows in (300, 2300):
+        check_route(l[:rows], 8)
     for kw in (dict(), dict(score="sigmoid"), dict(groups=8, topk_groups=3),
                dict(groups=8, topk_groups=3, group_top=2), dict(bias=torch.zeros(96))):
         check_route(l, 8, **kw)
@@ -72,14 +78,15 @@ def test_route_excluded_experts_and_odd_values():
     lowest = torch.finfo(torch.float32).min
     l[11, 4:] = lowest                # the type's lowest value is a value
     bias = torch.zeros(16)
-    check_route(l, 4)
-    check_route(l, 4, score="sigmoid")
-    check_route(l, 4, renormalize=False)
-    check_route(l, 4, groups=4, topk_groups=2)
-    check_route(l, 4, groups=4, topk_groups=2, group_top=2)
     bias[1], bias[2], bias[15] = -inf, nan, -0.5
-    check_route(l, 4, score="sigmoid", bias=bias)
-    check_route(l, 4, score="sigmoid", bias=bias, groups=4, topk_groups=2, group_top=2)
+    for rows in (l, l.repeat(180, 1)):
+        check_route(rows, 4)
+        check_route(rows, 4, score="sigmoid")
+        check_route(rows, 4, renormalize=False)
+        check_route(rows, 4, groups=4, topk_groups=2)
+        check_route(rows, 4, groups=4, topk_groups=2, group_top=2)
+        check_route(rows, 4, score="sigmoid", bias=bias)
+        check_route(rows, 4, score="sigmoid", bias=bias, groups=4, topk_groups=2, group_top=2)
 
 
 def test_route_empty_and_refusals():

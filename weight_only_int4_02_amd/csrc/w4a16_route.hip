@@ -14,8 +14,8 @@ namespace w4a16 {
 namespace {
 
 // ---------------------------------------------------------------------------
-// w4a16_route.  A row takes L = 16 lanes (up to 256 experts) or a whole wave;
-// lane l holds the V experts from l V on.
+// w4a16_route.  A row takes L = 16 or 64 lanes; lane l holds the V experts from
+// l V on.
 //
 // Which expert is larger must not hang on the rounding of an exponential:
 // without a bias, and with groups judged by their best expert alone, the
@@ -28,9 +28,10 @@ namespace {
 // expert's key is -infinity.  The chosen experts' scores are formed anew from
 // their logits at the end, one lane a slot.
 //
-// The kernel is bound by its instructions, not its bytes (8192 rows of 256
-// experts: 9 MB): with a wave to each row the reductions, the same for all of
-// a row's lanes, took 23 us; four rows to a wave share them.
+// The kernel is bound by its instructions and their latency, not its bytes
+// (8192 rows of 256 experts, 9 MB: 17 us, most of it the eight selections).  Few
+// rows take a wave each, for the latency; many share waves, since the
+// reductions are the same work for all of a row's lanes.
 // ---------------------------------------------------------------------------
 template <int CTRL>
 __device__ __forceinline__ int dpp(int v) {
@@ -47,6 +48,31 @@ __device__ __forceinline__ double dpp(double v) {
     const uint32_t hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(b >> 32));
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
+// op of the values D = 16 or 32 lanes apart: gfx950's swap of two registers'
+// odd and even halves, given the same register twice, leaves the even halves in
+// one result and the odd ones in the other.
+template <int D>
+__device__ __forceinline__ void halves(uint32_t v, uint32_t &even, uint32_t &odd) {
+    const auto r = D == 16 ? __builtin_amdgcn_permlane16_swap(v, v, false, false)
+                           : __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    even = r[0];
+    odd = r[1];
+}
+template <int D, typename T, typename F>
+__device__ __forceinline__ T op_rows(T v, F op) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t e, o;
+        halves<D>(__builtin_bit_cast(uint32_t, v), e, o);
+        return op(__builtin_bit_cast(T, e), __builtin_bit_cast(T, o));
+    } else {
+        const uint64_t b = __builtin_bit_cast(uint64_t, v);
+        uint32_t el, ol, eh, oh;
+        halves<D>((uint32_t)b, el, ol);
+        halves<D>((uint32_t)(b >> 32), eh, oh);
+        return op(__builtin_bit_cast(T, (uint64_t)eh << 32 | el),
+                  __builtin_bit_cast(T, (uint64_t)oh << 32 | ol));
+    }
+}
 // op over the L lanes of a row; every lane gets the result.
 template <int L, typename T, typename F>
 __device__ __forceinline__ T row_reduce(T v, F op) {
@@ -55,22 +81,20 @@ __device__ __forceinline__ T row_reduce(T v, F op) {
     v = op(v, dpp<0x141>(v));  // mirrored within 8
     v = op(v, dpp<0x140>(v));  // mirrored within 16
     if constexpr (L == 64) {
-        v = op(v, __shfl_xor(v, 16));
-        v = op(v, __shfl_xor(v, 32));
+        v = op_rows<16>(v, op);
+        v = op_rows<32>(v, op);
     }
     return v;
 }
 __device__ __forceinline__ float vmax(float a, float b) { return fmaxf(a, b); }
 __device__ __forceinline__ double vmax(double a, double b) { return fmax(a, b); }
 
-template <int DT>
-__device__ __forceinline__ float load_logit(const void *p, int64_t at) {
-    if constexpr (DT == W4A16_LOGITS_F32)
-        return ((const float *)p)[at];
-    else if constexpr (DT == W4A16_LOGITS_BF16)
-        return bf16_bits_to_float(((const uint16_t *)p)[at]);
-    else
-        return (float)((const _Float16 *)p)[at];
+__device__ __forceinline__ float load_logit(const RouteArgs &a, int64_t at) {
+    if (a.dtype == W4A16_LOGITS_F32)
+        return ((const float *)a.logits)[at];
+    if (a.dtype == W4A16_LOGITS_BF16)
+        return bf16_bits_to_float(((const uint16_t *)a.logits)[at]);
+    return (float)((const _Float16 *)a.logits)[at];
 }
 __device__ __forceinline__ float clean_logit(float x) {
     return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
@@ -120,7 +144,7 @@ __device__ __forceinline__ Key score_of(float l, float top, bool sigmoid) {
 
 constexpr int kRouteThreads = 256;
 
-template <int V, int L, bool WIDE, int DT>
+template <int V, int L, bool WIDE>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     using Key = std::conditional_t<WIDE, double, float>;
     constexpr int ROWS = kRouteThreads / L;
@@ -138,18 +162,26 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     float lg[V];
     float top = -INFINITY;
     const int own = a.E - l * V;      // the lane's experts that there are
-    if (a.E == V * L) {
+    auto load_as = [&](auto of) __attribute__((always_inline)) {
+        if (a.E == V * L) {
 #pragma unroll
-        for (int v = 0; v < V; v++)
-            lg[v] = load_logit<DT>(a.logits, base + l * V + v);
-    } else {
-        // (past the row's end, its last logit is loaded and dropped)
+            for (int v = 0; v < V; v++)
+                lg[v] = of(base + l * V + v);
+        } else {
+            // (past the row's end, its last logit is loaded and dropped)
 #pragma unroll
-        for (int v = 0; v < V; v++) {
-            const float x = load_logit<DT>(a.logits, base + min(l * V + v, a.E - 1));
-            lg[v] = v < own ? x : -INFINITY;
+            for (int v = 0; v < V; v++) {
+                const float x = of(base + min(l * V + v, a.E - 1));
+                lg[v] = v < own ? x : -INFINITY;
+            }
         }
-    }
+    };
+    if (a.dtype == W4A16_LOGITS_F32)
+        load_as([&](int64_t at) { return ((const float *)a.logits)[at]; });
+    else if (a.dtype == W4A16_LOGITS_BF16)
+        load_as([&](int64_t at) { return bf16_bits_to_float(((const uint16_t *)a.logits)[at]); });
+    else
+        load_as([&](int64_t at) { return (float)((const _Float16 *)a.logits)[at]; });
 #pragma unroll
     for (int v = 0; v < V; v++) {
         lg[v] = clean_logit(lg[v]);
@@ -205,7 +237,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             take(best, second, b2);
             take(best, second, s2);
             const Key x = a.group_top == 2 && second != none ? best + second : best;
-            const Key y = __shfl(x, (int)(threadIdx.x & 48) + ((2 * l) & 15));
+            const Key y = __shfl(x, (int)(threadIdx.x & (64 - L)) + ((2 * l) & (L - 1)));
             value[0] = l < a.n_groups ? y : none;
 #pragma unroll
             for (int q = 1; q < NQ; q++)
@@ -303,7 +335,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int n = 0; n < NS; n++) {
         const float x =
-            id[n] < 0 ? -INFINITY : clean_logit(load_logit<DT>(a.logits, base + id[n]));
+            id[n] < 0 ? -INFINITY : clean_logit(load_logit(a, base + id[n]));
         w[n] = score_of<Key>(x, top, sig) * inv;
         total += w[n];
     }
@@ -323,24 +355,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
     }
 }
 
-template <int V, int L, bool WIDE>
-void launch_route_typed(const RouteArgs &a, int dt, hipStream_t st) {
+template <int V, int L>
+void launch_route_rows(const RouteArgs &a, bool wide, hipStream_t st) {
     constexpr int ROWS = kRouteThreads / L;
     const dim3 grid((unsigned)((a.T + ROWS - 1) / ROWS)), block(kRouteThreads);
-    if (dt == W4A16_LOGITS_F32)
-        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_F32>), grid, block, 0, st, a);
-    else if (dt == W4A16_LOGITS_BF16)
-        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_BF16>), grid, block, 0, st, a);
-    else
-        hipLaunchKernelGGL((route_kernel<V, L, WIDE, W4A16_LOGITS_F16>), grid, block, 0, st, a);
-}
-
-template <int V, int L>
-void launch_route_wide(const RouteArgs &a, int dt, bool wide, hipStream_t st) {
     if (wide)
-        launch_route_typed<V, L, true>(a, dt, st);
+        hipLaunchKernelGGL((route_kernel<V, L, true>), grid, block, 0, st, a);
     else
-        launch_route_typed<V, L, false>(a, dt, st);
+        hipLaunchKernelGGL((route_kernel<V, L, false>), grid, block, 0, st, a);
 }
 
 // ---------------------------------------------------------------------------
@@ -517,21 +539,28 @@ void launch_combine(const CombineArgs &a, hipStream_t st) {
 
 }  // namespace
 
-int launch_route(const RouteArgs &a, int logits_dtype, void *stream) {
+int launch_route(const RouteArgs &a, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
     const bool wide = a.bias != nullptr || (a.topk_groups < a.n_groups && a.group_top == 2);
-    if (a.E <= 16)
-        launch_route_wide<1, 16>(a, logits_dtype, wide, st);
+    // Up to two waves a SIMD, a wave to a row: 61 rows of 160 experts 7.4 us,
+    // 8.6 with 16 lanes a row.  Above, 16 lanes: 8192 rows of 256 experts
+    // 17.2 us, 21.0 with 32 lanes, 23 with 64.
+    const bool few = a.T <= 2048;
+    if (a.E <= 256 && !few)
+        a.E <= 16    ? launch_route_rows<1, 16>(a, wide, st)
+        : a.E <= 64  ? launch_route_rows<4, 16>(a, wide, st)
+        : a.E <= 128 ? launch_route_rows<8, 16>(a, wide, st)
+                     : launch_route_rows<16, 16>(a, wide, st);
     else if (a.E <= 64)
-        launch_route_wide<4, 16>(a, logits_dtype, wide, st);
+        launch_route_rows<1, 64>(a, wide, st);
     else if (a.E <= 128)
-        launch_route_wide<8, 16>(a, logits_dtype, wide, st);
+        launch_route_rows<2, 64>(a, wide, st);
     else if (a.E <= 256)
-        launch_route_wide<16, 16>(a, logits_dtype, wide, st);
+        launch_route_rows<4, 64>(a, wide, st);
     else if (a.E <= 512)
-        launch_route_wide<8, 64>(a, logits_dtype, wide, st);
+        launch_route_rows<8, 64>(a, wide, st);
     else
-        launch_route_wide<16, 64>(a, logits_dtype, wide, st);
+        launch_route_rows<16, 64>(a, wide, st);
     return (int)hipGetLastError();
 }
 

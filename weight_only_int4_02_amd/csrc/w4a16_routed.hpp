@@ -17,9 +17,9 @@ struct RouteArgs {
     float *weights;
     int T, E, k, n_groups, topk_groups, group_top;
     float scale;
-    int sigmoid, renormalize;
+    int sigmoid, renormalize, dtype;
 };
-int launch_route(const RouteArgs &a, int logits_dtype, void *stream);
+int launch_route(const RouteArgs &a, void *stream);
 
 // ---- experts ---------------------------------------------------------------
 // Rows (t, j) of the [T][k] slots are numbered flat, t k + j.  A tile is up to

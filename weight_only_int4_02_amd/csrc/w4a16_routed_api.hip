@@ -59,9 +59,10 @@ int32_t w4a16_route(const void *logits, int32_t logits_dtype, int64_t T, int64_t
     a.topk_groups = topk_groups;
     a.group_top = group_top;
     a.scale = scale;
+    a.dtype = logits_dtype;
     a.sigmoid = (flags & W4A16_ROUTE_SIGMOID) ? 1 : 0;
     a.renormalize = (flags & W4A16_ROUTE_RENORMALIZE) ? 1 : 0;
-    return finish_launch("w4a16_route", launch_route(a, logits_dtype, stream));
+    return finish_launch("w4a16_route", launch_route(a, stream));
 }
 
 int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *ids,
