@@ -154,6 +154,9 @@ CASES = [
     (130, 8, 2, 128, 136, 257, 32), (150, 6, 2, 392, 512, 260, 64), (129, 4, 1, 648, 72, 300, 256),
     (333, 2, 1, 264, 640, 516, 32), (257, 3, 3, 1160, 264, 131, 64), (500, 2, 1, 512, 1032, 640, 256),
     (140, 1, 1, 128, 128, 16, 128), (700, 5, 2, 640, 200, 1100, 128),
+    # more slots than workgroups, with a last round cut into half slots and
+    # tiles of few rows among the whole ones
+    (1500, 4, 1, 128, 8192, 264, 128), (1400, 4, 1, 256, 136, 20000, 64), (900, 3, 1, 136, 10000, 9000, 32),
 ]
 
 
