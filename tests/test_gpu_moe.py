@@ -149,6 +149,9 @@ CASES = [
     (7, 4, 2, 512, 256, 257, 64), (16, 4, 4, 256, 384, 256, 32), (64, 2, 1, 136, 72, 17, 32),
     (33, 8, 2, 520, 200, 264, 256), (40, 2, 2, 256, 264, 256, 128), (100, 16, 4, 384, 128, 130, 128),
     (200, 3, 1, 1024, 104, 64, 64), (300, 4, 4, 256, 256, 512, 128),
+    # one token: many slots, partial stages, and an activation image too large
+    (1, 16, 8, 264, 200, 100, 32), (1, 4, 4, 1160, 648, 257, 64), (1, 4, 4, 128, 11008, 64, 128),
+    (1, 3, 2, 4096, 1408, 2048, 256), (1, 32, 32, 128, 136, 48, 128),
     # the compute-bound kernel: 64-row and 128-row tiles, every group size,
     # K of one, few and many stages, ragged columns and a partial last stage
     (130, 8, 2, 128, 136, 257, 32), (150, 6, 2, 392, 512, 260, 64), (129, 4, 1, 648, 72, 300, 256),
@@ -187,6 +190,21 @@ def test_experts_rows_without_an_expert(T):
     none = moe.experts(Xc, torch.full_like(idc, -1), wc, gu, dn)
     assert none.shape == y.shape and not none.any()
     assert tuple(moe.experts(Xc[:0], idc[:0], wc[:0], gu, dn).shape) == (0, 128)
+
+
+@pytest.mark.parametrize("ids", [[2, 2, 0], [-1, 3, 99], [-1, 4, -5], [3, -1, 3]])
+def test_one_token(ids):
+    """A single row's form: an expert twice, slots without one (whose weights,
+    NaN here, are not looked at), and none at all."""
+    case = draw(1, 4, 3, 520, 264, 100, 128, "f16", False, seed=7)
+    case[1][:] = torch.tensor(ids)
+    for j, e in enumerate(ids):
+        case[2][0, j] = 0.25 + j if 0 <= e < 4 else float("nan")
+    X, i, w, gu, dn = on_gpu(case, 128)
+    y = moe.experts(X, i, w, gu, dn)
+    want, bound = ref.experts(case[0], case[1], torch.nan_to_num(case[2], 0.0), *case[3:], 128)
+    assert bool(((y.cpu().double() - want).abs() <= bound).all())
+    assert y.any() == any(0 <= e < 4 for e in ids)
 
 
 @pytest.mark.parametrize("T,all_one", [(64, True), (300, True), (300, False)])

@@ -23,6 +23,7 @@ SOURCES = ["w4a16_host.cpp", "w4a16_api.hip", "w4a16_kernels.hip", "w4a16_gemm.h
            "w4a16_large.hip", "w4a16_large_bf16.hip", "w4a16_quantize.hip",
            "w4a16_stream.hip", "w4a16_routed_host.cpp", "w4a16_routed_api.hip",
            "w4a16_route.hip", "w4a16_experts_small.hip", "w4a16_experts_small_bf16.hip",
+           "w4a16_experts_one.hip", "w4a16_experts_one_bf16.hip",
            "w4a16_experts_large.hip", "w4a16_experts_large_bf16.hip",
            "w4a16_lora.hip",
            "w4a16_small_jpg1_lora.hip", "w4a16_small_jpg2_lora.hip", "w4a16_small_jpg4_lora.hip",

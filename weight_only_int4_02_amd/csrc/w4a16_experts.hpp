@@ -49,6 +49,19 @@ __device__ __forceinline__ bf8_t dequant_word_bf16_fma(uint32_t w, Bf16Fma g) {
     return __builtin_bit_cast(bf8_t, o);
 }
 
+// One MFMA of 16 x 16 results with the weight operand formed from a packed word.
+template <bool BF>
+__device__ __forceinline__ f4_t expert_mfma(u4_t x, uint32_t word, uint32_t z, uint32_t sbits,
+                                            uint32_t magic, f4_t c) {
+    if constexpr (BF) {
+        return mfma16x16x32_bf16(__builtin_bit_cast(bf8_t, x),
+                                 dequant_word_bf16_fma(word, bf16_fma(sbits, z)), c);
+    } else {
+        return mfma16x16x32(__builtin_bit_cast(h8_t, x),
+                            dequant_word(word, zero_pair(z), scale_pair(sbits), magic), c);
+    }
+}
+
 // mfma8_dequant_bf16 with that form: eight MFMAs with the next word's
 // dequantization between them, four vector instructions after each of the
 // first six, and the same FORMs and hazards.

@@ -37,6 +37,7 @@ struct ExpertTile {
 };
 
 struct ExpertsPlan {
+    int one;             // a single token: the kernels of w4a16_experts_one.inc
     int direct;          // no plan kernel
     int large;           // the compute-bound kernel
     int mt;              // small kernel: 16-row activation tiles per workgroup
@@ -79,6 +80,8 @@ int launch_experts_small(const ExpertsArgs &a, const ExpertsPlan &p, bool gated,
 int launch_experts_small_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_large(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_large_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
+int launch_experts_one(const ExpertsArgs &a, const float *weights, bool gated, void *stream);
+int launch_experts_one_bf16(const ExpertsArgs &a, const float *weights, bool gated, void *stream);
 int launch_experts_combine(const CombineArgs &a, void *stream);
 
 // ---- adapters ----------------------------------------------------------------

@@ -106,6 +106,14 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
         a->k = k;
         a->direct = p.direct;
     }
+    if (p.one) {
+        const auto one = bf ? launch_experts_one_bf16 : launch_experts_one;
+        dn.Y = Y;
+        e = one(gu, weights, true, stream);
+        if (!e)
+            e = one(dn, weights, false, stream);
+        return finish_launch("w4a16_experts", e);
+    }
     const auto launch = p.large ? (bf ? launch_experts_large_bf16 : launch_experts_large)
                                 : (bf ? launch_experts_small_bf16 : launch_experts_small);
     if (!e)

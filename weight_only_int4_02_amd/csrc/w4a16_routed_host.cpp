@@ -65,10 +65,16 @@ int32_t check_lora_shape(int64_t N, int64_t K, int64_t n, int32_t r, int32_t n_p
 ExpertsPlan plan_experts(int64_t T, int k, int64_t K, int64_t I, int64_t D, int64_t E, int32_t g,
                          uint32_t flags) {
     ExpertsPlan p;
-    (void)K;
-    (void)g;
-    (void)flags;
     const int64_t R = T * k;
+    // One token's activations, scales and zero words stay in LDS (1 KiB
+    // chunks, of every slot in the second product) where they leave room for
+    // two workgroups on a compute unit.
+    const Geom gu = make_geom(1, I, K, g, flags), dn = make_geom(1, D, I, g, flags);
+    auto image = [](const Geom &q, int tiles) {
+        return (q.KT * 256 + 1023) / 1024 +
+               tiles * ((q.G * 32 + 1023) / 1024 + (q.sym ? 0 : (q.GW * 64 + 1023) / 1024));
+    };
+    p.one = T == 1 && image(gu, 2) <= 72 && k * image(dn, 1) <= 72;
     p.direct = R <= kDirectRows;
     p.mt = R <= 16 * E ? 1 : 4;
     p.large = !p.direct && R > 16 * E;
