@@ -78,7 +78,8 @@ int32_t w4a16_check_route_args(const void *logits, int32_t logits_dtype, int64_t
  * workspace: w4a16_experts_workspace_size bytes (no fill needed); calls that
  * may run at the same time need separate ones.
  * Limits: 1 <= E <= 1024, 1 <= k <= 32, T <= 2^20, T * k <= 2^22, X below
- * 2 GiB, and each expert's 2 I K and D I below 2^32 elements.
+ * 2 GiB, each expert's 2 I K and D I below 2^32 elements, I and D below
+ * 2^22; W4A16_BF16: scales below 2^124 in magnitude (z s is formed in fp32).
  * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE, W4A16_ERR_GROUP, W4A16_ERR_FLAGS,
  * W4A16_ERR_ALIGN, W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_experts_workspace_size(int64_t T, int32_t k, int64_t K, int64_t I, int64_t D,
@@ -107,9 +108,9 @@ int32_t w4a16_check_experts_args(const uint16_t *X, int64_t T, int64_t K, const 
  * q, k and v); part p uses rows p r .. (p+1) r - 1 of A_a.
  *   A       16-bit [n][n_parts * r][K];   B 16-bit [n][N][r];
  *   scales  fp32 [n];   adapter_ids int32 [M].
- * All sums are fp32 (the low-rank values X . A^T included, where M is large
- * they feed the second product as pairs of bf16, 16 bits of them), and Y is
- * rounded once.  part_sizes is read on the host during the call.
+ * All sums are fp32; the low-rank values scales[a] X . A_a^T enter the second
+ * product as pairs of 16-bit values (16 bits of each in bf16, 22 of the row's
+ * largest in fp16, whatever their range), and Y is rounded once.  part_sizes is read on the host during the call.
  * workspace: w4a16_gemm_lora_workspace_size bytes (no fill needed); calls
  * that may run at the same time need separate ones.
  * Limits: those of w4a16_gemm, n <= 65536, r a multiple of 8 up to 256,

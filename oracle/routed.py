@@ -124,7 +124,8 @@ def gemm_lora(X, W, A, B, scales, ids, sizes):
     Bound: the projection is a 32-bit sum of K products whose weights may be
     unrounded (half a 16-bit step of each); the low-rank values are 32-bit sums
     of K products, and enter a sum of r products as 16 significant bits (2^-16
-    of each product, three parts)."""
+    of each product; in fp16 22 bits of the largest of a row's 32 ranks, which
+    is 2^-22 of the sum of all of them)."""
     dt = X.dtype
     u, tiny = torch.finfo(dt).eps / 2, torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
     Xd, K = X.double(), X.shape[1]
@@ -145,7 +146,8 @@ def gemm_lora(X, W, A, B, scales, ids, sizes):
             sc = scales[a].double()
             Y[rows, c0:c1] += sc * (s @ Bp.T)
             err[rows, c0:c1] += sc.abs() * (es @ Bp.abs().T +
-                                            (3 * 2.0 ** -16 + 4 * r * U32) * ((s.abs() + es) @ Bp.abs().T))
+                                            (3 * 2.0 ** -16 + 4 * r * U32) * ((s.abs() + es) @ Bp.abs().T) +
+                                            2.0 ** -21 * (s.abs() + es).amax(1, keepdim=True) * Bp.abs().sum(1))
             c0 = c1
     err = err + 2 * U32 * (Y.abs() + err)
     return Y, err + u * (Y.abs() + err) + tiny

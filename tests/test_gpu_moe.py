@@ -151,7 +151,7 @@ CASES = [
     (200, 3, 1, 1024, 104, 64, 64), (300, 4, 4, 256, 256, 512, 128),
     # one token: many slots, partial stages, and an activation image too large
     (1, 16, 8, 264, 200, 100, 32), (1, 4, 4, 1160, 648, 257, 64), (1, 4, 4, 128, 11008, 64, 128),
-    (1, 3, 2, 4096, 1408, 2048, 256), (1, 32, 32, 128, 136, 48, 128),
+    (1, 3, 2, 4096, 1408, 2048, 256), (1, 32, 32, 128, 136, 48, 128), (1, 2, 2, 128, 14336, 32, 128),
     # the compute-bound kernel: 64-row and 128-row tiles, every group size,
     # K of one, few and many stages, ragged columns and a partial last stage
     (130, 8, 2, 128, 136, 257, 32), (150, 6, 2, 392, 512, 260, 64), (129, 4, 1, 648, 72, 300, 256),

@@ -55,8 +55,11 @@ class Adapters:
     scales: torch.Tensor   # fp32 [n]
     n: int
     r: int
-    sizes: Sequence[int]   # columns of each part
-    c_sizes: ctypes.Array = field(repr=False, default=None)
+    c_sizes: ctypes.Array = field(repr=False)   # columns of each part
+
+    @property
+    def sizes(self):
+        return list(self.c_sizes)
 
     @property
     def K(self) -> int:
@@ -96,14 +99,14 @@ def adapters(A: torch.Tensor, B: torch.Tensor, scales: torch.Tensor,
         A = torch.cat([A, A.new_zeros((n, parts, pad, K))], 2)
         B = torch.cat([B, B.new_zeros((n, N, pad))], 2)
         r += pad
-    return Adapters(A.reshape(n, parts * r, K).contiguous(), B.contiguous(), scales, n, r, sizes,
+    return Adapters(A.reshape(n, parts * r, K).contiguous(), B.contiguous(), scales, n, r,
                     (ctypes.c_int64 * parts)(*sizes))
 
 
 def gemm_lora_workspace_size(M: int, w: PackedWeight, ad: Adapters, flags: int = 0) -> int:
     b = ctypes.c_size_t()
     _raise(_routed().w4a16_gemm_lora_workspace_size(M, w.N, w.K, w.g, w.flags | flags,
-                                                    len(ad.sizes), ad.r, ctypes.byref(b)),
+                                                    len(ad.c_sizes), ad.r, ctypes.byref(b)),
            "w4a16_gemm_lora_workspace_size")
     return b.value
 
@@ -130,7 +133,7 @@ def gemm_lora(X: torch.Tensor, w: PackedWeight, ad: Adapters, ids: torch.Tensor,
         raise TypeError("X, the weight's scales and the adapters must share one 16-bit format")
     if ids.shape[0] != M:
         raise ValueError("ids must be [M]")
-    n, r, parts = ad.n, ad.r, len(ad.sizes)
+    n, r, parts = ad.n, ad.r, len(ad.c_sizes)
     check(ad.A, "adapters.A", dtype, 3, device)
     check(ad.B, "adapters.B", dtype, 3, device)
     check(ad.scales, "adapters.scales", torch.float32, 1, device)

@@ -176,6 +176,8 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     if n % 16 == 0 and m * n <= 1 << 26 and m * n * K <= 1 << 34:
         # whole row tiles: the matrices one below the other are one weight
         zp = None if zeros is None else pack(zeros.reshape(m * n, G))
+        if scales.data_ptr() % 16:
+            scales = scales.clone()
         w = repack(pack(codes.reshape(m * n, K)), scales.reshape(m * n, G), zp, K, g,
                    symmetric=zeros is None, partial=partial)
         return ExpertWeight(w.q, w.s, w.z, E, n, K, g, flags, gated)
