@@ -306,3 +306,53 @@ def test_router_and_experts_together(T, E):
         eager = layer(x, l)
         torch.cuda.synchronize()
         assert torch.equal(eager.reshape(T, K), out)
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls without a workspace of their own, on two streams that nothing
+    orders: each has its own block, eager and in two graphs replayed in turn."""
+    cases = [draw(T, 8, 3, 256, 128, 256, 64, "f16", False, seed=20 + T) for T in (150, 21)]
+    args = [on_gpu(c, 64) for c in cases]
+    want = [moe.experts(*a) for a in args]
+    streams = [torch.cuda.Stream() for _ in args]
+    outs = [torch.empty_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        got = []
+        for st, a in zip(streams, args):
+            with torch.cuda.stream(st):
+                got.append(moe.experts(*a))
+        torch.cuda.synchronize()
+        for y, w in zip(got, want):
+            assert torch.equal(y, w)
+    graphs = []
+    for st, a, o in zip(streams, args, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.stream(st), torch.cuda.graph(graphs[-1], stream=st):
+            moe.experts(*a, out=o)
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for st, graph in zip(streams, graphs):
+            with torch.cuda.stream(st):
+                graph.replay()
+        torch.cuda.synchronize()
+        for y, w, a in zip(outs, want, args):
+            assert torch.equal(y, w)
+            assert torch.equal(moe.experts(*a), w)
+        torch.cuda.synchronize()
+
+
+def test_sizes_that_are_refused_before_memory_is_taken():
+    logits = torch.zeros((1 << 10, 8), device="cuda")
+    for k in (0, -1, 9, 33, 1 << 40, (1 << 32) + 1):
+        with pytest.raises(ValueError):
+            moe.route(logits, k)
+    codes = torch.zeros((2, 32, 64), dtype=torch.uint8, device="cuda")
+    scales = torch.ones((2, 32, 2), dtype=torch.float16, device="cuda")
+    for g in (0, -32):
+        with pytest.raises(ValueError):
+            moe.expert_weight(codes, scales, None, g)
+    with pytest.raises(ValueError):
+        moe.expert_weight(codes, scales.cpu(), None, 32)

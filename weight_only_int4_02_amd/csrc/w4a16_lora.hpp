@@ -111,6 +111,7 @@ template <bool BF, int W, int NB, int MT, int P>
 struct LoraPart {
     // items in flight: as many as their registers (8 P S values, 4 P NB of B)
     // leave room for
+    static_assert(MT <= 2, "an item's row tile is 0 or 1");
     static constexpr int BATCH = P * NB <= 2 ? 4 : P * NB <= 6 ? 2 : 1;
     struct Item {
         int t;             // row tile, -1: none

@@ -110,6 +110,8 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax",
     device = logits.get_device()
     if score not in ("softmax", "sigmoid"):
         raise ValueError("score must be 'softmax' or 'sigmoid'")
+    if not 0 < k <= MAX_K:   # (before memory is taken for it)
+        raise ValueError(f"k must be 1 to {MAX_K}")
     T, E = logits.shape
     if bias is not None:
         check(bias, "bias", torch.float32, 1, device)
@@ -121,8 +123,8 @@ def route(logits: torch.Tensor, k: int, score: str = "softmax",
         _raise(_routed().w4a16_check_route_args(16, _LOGITS[logits.dtype], 1, E, _at(bias), k,
                                                 groups, topk_groups, group_top, scale, 0, 16, 16),
                "w4a16_route")
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
-    weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
     if T:
         flags = (_ROUTE_SIGMOID if score == "sigmoid" else 0) | (_ROUTE_RENORMALIZE if renormalize else 0)
         _raise(_routed().w4a16_route(logits.data_ptr(), _LOGITS[logits.dtype], T, E, _at(bias), k,
@@ -155,12 +157,16 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     multiple of g has a partial last group."""
     _need(codes, "codes", torch.uint8, 3)
     bf = _need16(scales, "scales", 3)
+    device = codes.get_device()
+    check(scales, "scales", scales.dtype, 3, device)
+    if g < 1:
+        raise ValueError("g must be 32, 64, 128 or 256")
     E, N, K = codes.shape
     G = -(-K // g)
     if tuple(scales.shape) != (E, N, G):
         raise ValueError("scales must be [E, N, ceil(K/g)]")
     if zeros is not None:
-        _need(zeros, "zeros", torch.uint8, 3)
+        check(zeros, "zeros", torch.uint8, 3, device)
         if tuple(zeros.shape) != (E, N, G):
             raise ValueError("zeros must be [E, N, ceil(K/g)]")
     if E < 1 or E > MAX_EXPERTS:
@@ -168,7 +174,7 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     parts = 2 if gated else 1
     if N % parts:
         raise ValueError("a gated weight has an even number of rows")
-    stream_of(codes.get_device())
+    stream_of(device)
     n = N // parts
     flags = (SYMMETRIC if zeros is None else 0) | (PARTIAL_LAST_GROUP if K % g else 0) | (BF16 if bf else 0)
     m = E * parts
