@@ -356,3 +356,20 @@ def test_sizes_that_are_refused_before_memory_is_taken():
             moe.expert_weight(codes, scales, None, g)
     with pytest.raises(ValueError):
         moe.expert_weight(codes, scales.cpu(), None, 32)
+
+
+@pytest.mark.parametrize("n,symmetric", [(40, False), (16, True), (33, True)])
+def test_expert_weight_is_each_matrix_repacked(n, symmetric):
+    """The matrices in the device layout, one after the other, also where their
+    rows end inside a tile."""
+    E, K, g = 3, 200, 64
+    codes = torch.randint(0, 16, (E, 2 * n, K), generator=gen(n), dtype=torch.uint8).cuda()
+    scales = torch.rand((E, 2 * n, 4), generator=gen(n + 1)).half().cuda()
+    zeros = None if symmetric else torch.randint(0, 16, (E, 2 * n, 4), generator=gen(n + 2), dtype=torch.uint8).cuda()
+    got = moe.expert_weight(codes, scales, zeros, g, gated=True)
+    one = [w4.repack(w4.pack(codes[e, r].contiguous()), scales[e, r].clone(),
+                     None if symmetric else w4.pack(zeros[e, r].contiguous()), K, g, symmetric=symmetric, partial=True)
+           for e in range(E) for r in (slice(0, n), slice(n, 2 * n))]
+    assert torch.equal(got.q.flatten(), torch.cat([w.q for w in one]))
+    assert torch.equal(got.s.flatten(), torch.cat([w.s for w in one]))
+    assert symmetric or torch.equal(got.z.flatten(), torch.cat([w.z for w in one]))

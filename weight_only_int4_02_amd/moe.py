@@ -175,31 +175,35 @@ def expert_weight(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[tor
     if N % parts:
         raise ValueError("a gated weight has an even number of rows")
     stream_of(device)
-    n = N // parts
+    n, m = N // parts, E * parts
     flags = (SYMMETRIC if zeros is None else 0) | (PARTIAL_LAST_GROUP if K % g else 0) | (BF16 if bf else 0)
-    m = E * parts
-    partial = K % g != 0
-    if n % 16 == 0 and m * n <= 1 << 26 and m * n * K <= 1 << 34:
-        # whole row tiles: the matrices one below the other are one weight
-        zp = None if zeros is None else pack(zeros.reshape(m * n, G))
-        if scales.data_ptr() % 16:
-            scales = scales.clone()
-        w = repack(pack(codes.reshape(m * n, K)), scales.reshape(m * n, G), zp, K, g,
-                   symmetric=zeros is None, partial=partial)
-        return ExpertWeight(w.q, w.s, w.z, E, n, K, g, flags, gated)
-    qb, sb, zb = repack_size(n, K, g, flags)
-    q = torch.empty((m, qb), dtype=torch.uint8, device=codes.device)
-    s = torch.empty((m, sb // 2), dtype=scales.dtype, device=codes.device)
-    z = None if zeros is None else torch.empty((m, zb // 4), dtype=torch.int32, device=codes.device)
-    for j in range(m):
-        rows = (j // parts, slice((j % parts) * n, (j % parts + 1) * n))
-        # (a clone: one matrix's scales need not begin at a multiple of 16 bytes)
-        w = repack(pack(codes[rows]), scales[rows].clone(),
-                   None if zeros is None else pack(zeros[rows]), K, g, symmetric=zeros is None,
-                   partial=partial)
-        q[j], s[j] = w.q, w.s
-        if z is not None:
-            z[j] = w.z
+    repack_size(n, K, g, flags)   # one matrix's own limits
+    pad = -n % 16
+
+    def whole_tiles(t, j0, j1):
+        """Matrices j0 .. j1 - 1 one below the other, each with rows of zeros up
+        to a whole row tile: repack()ed together, they are laid out as one by one."""
+        t = t.reshape(m, n, -1)[j0:j1]
+        if pad:
+            t = torch.nn.functional.pad(t, (0, 0, 0, pad))
+        return t.reshape((j1 - j0) * (n + pad), -1)
+
+    # as many matrices at once as repack() takes rows and weights
+    step = max(1, min(m, (1 << 26) // (n + pad), (1 << 34) // ((n + pad) * K)))
+    done = []
+    for j0 in range(0, m, step):
+        j1 = min(m, j0 + step)
+        rows = whole_tiles(scales, j0, j1)
+        if rows.data_ptr() % 16:
+            rows = rows.clone()
+        done.append(repack(pack(whole_tiles(codes, j0, j1)), rows,
+                           None if zeros is None else pack(whole_tiles(zeros, j0, j1)), K, g,
+                           symmetric=zeros is None, partial=K % g != 0))
+    if len(done) == 1:
+        q, s, z = done[0].q, done[0].s, done[0].z
+    else:
+        q, s = torch.cat([w.q for w in done]), torch.cat([w.s for w in done])
+        z = None if zeros is None else torch.cat([w.z for w in done])
     return ExpertWeight(q, s, z, E, n, K, g, flags, gated)
 
 
