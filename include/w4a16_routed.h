@@ -80,8 +80,9 @@ int32_t w4a16_check_route_args(const void *logits, int32_t logits_dtype, int64_t
  * Limits: 1 <= E <= 1024, 1 <= k <= 32, T <= 2^20, T * k <= 2^22, X below
  * 2 GiB, each expert's 2 I K and D I below 2^32 elements, I and D below
  * 2^22; W4A16_BF16: scales below 2^124 in magnitude (z s is formed in fp32).
- * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE, W4A16_ERR_GROUP, W4A16_ERR_FLAGS,
- * W4A16_ERR_ALIGN, W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y overlaps X, ids or
+ * weights), W4A16_ERR_GROUP, W4A16_ERR_FLAGS, W4A16_ERR_ALIGN,
+ * W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_experts_workspace_size(int64_t T, int32_t k, int64_t K, int64_t I, int64_t D,
                                      int64_t E, int32_t g, uint32_t flags, size_t *bytes);
 int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *ids,
@@ -116,7 +117,7 @@ int32_t w4a16_check_experts_args(const uint16_t *X, int64_t T, int64_t K, const 
  * Limits: those of w4a16_gemm, n <= 65536, r a multiple of 8 up to 256,
  * n_parts <= W4A16_LORA_MAX_PARTS, part sizes positive with sum N, one
  * adapter's A below 2 GiB.
- * Errors: as w4a16_gemm. */
+ * Errors: as w4a16_gemm (Y must not overlap adapter_ids either). */
 int32_t w4a16_gemm_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t g,
                                        uint32_t flags, int32_t n_parts, int32_t r,
                                        size_t *bytes);

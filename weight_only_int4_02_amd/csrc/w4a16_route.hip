@@ -226,18 +226,24 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             best = vmax(best, x);
         };
         __shared__ Key ks[ROWS][V * L + V * L / 16];
-        if (L == 16 && size == 2 * V) {
-            // a group is two lanes' keys: they meet by one move, and lane q
-            // fetches group q's value
+        if (size % V == 0) {
+            // a group is n whole lanes' keys: after the step of d lanes, a
+            // lane holds the two best of its 2 d and those behind them in its
+            // group, and lane q fetches group q's value from its first lane
+            // (8192 rows of 512 experts in 8 groups, through LDS as below:
+            // 41.6 us, so 29.2; 61 rows of 160 in 8: 7.1, 5.0)
+            const int n = size / V, behind = n - 1 - l % n;
             Key best = none, second = none;
 #pragma unroll
             for (int v = 0; v < V; v++)
                 take(best, second, key[v]);
-            const Key b2 = dpp<0xB1>(best), s2 = dpp<0xB1>(second);
-            take(best, second, b2);
-            take(best, second, s2);
+            for (int d = 1; d < n; d *= 2) {
+                const Key b2 = __shfl_down(best, d), s2 = __shfl_down(second, d);
+                take(best, second, d <= behind ? b2 : none);
+                take(best, second, d <= behind ? s2 : none);
+            }
             const Key x = a.group_top == 2 && second != none ? best + second : best;
-            const Key y = __shfl(x, (int)(threadIdx.x & (64 - L)) + ((2 * l) & (L - 1)));
+            const Key y = __shfl(x, (int)(threadIdx.x & (64 - L)) + min(l * n, L - 1));
             value[0] = l < a.n_groups ? y : none;
 #pragma unroll
             for (int q = 1; q < NQ; q++)
@@ -542,9 +548,10 @@ void launch_combine(const CombineArgs &a, hipStream_t st) {
 int launch_route(const RouteArgs &a, void *stream) {
     const hipStream_t st = (hipStream_t)stream;
     const bool wide = a.bias != nullptr || (a.topk_groups < a.n_groups && a.group_top == 2);
-    // Up to two waves a SIMD, a wave to a row: 61 rows of 160 experts 7.4 us,
-    // 8.6 with 16 lanes a row.  Above, 16 lanes: 8192 rows of 256 experts
-    // 17.2 us, 21.0 with 32 lanes, 23 with 64.
+    // Up to two waves a SIMD, a wave to a row: 2048 rows of 256 experts in
+    // groups, with a bias, 8.6 us, 12.3 with 16 lanes a row; of 64 experts 6.7
+    // either way.  Above, 16 lanes: 4096 rows of 64 experts 6.9 us, 9.8 with a
+    // wave a row; 8192 of 256 experts 17 us, 21 with 32 lanes, 23 with 64.
     const bool few = a.T <= 2048;
     if (a.E <= 256 && !few)
         a.E <= 16    ? launch_route_rows<1, 16>(a, wide, st)
