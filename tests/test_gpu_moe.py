@@ -373,3 +373,18 @@ def test_expert_weight_is_each_matrix_repacked(n, symmetric):
     assert torch.equal(got.q.flatten(), torch.cat([w.q for w in one]))
     assert torch.equal(got.s.flatten(), torch.cat([w.s for w in one]))
     assert symmetric or torch.equal(got.z.flatten(), torch.cat([w.z for w in one]))
+
+
+@pytest.mark.parametrize("E,groups,topk,k", [(264, 8, 3, 6), (512, 4, 2, 8), (500, 5, 2, 4), (1000, 8, 4, 8), (1024, 64, 9, 32),
+                                             (1024, 2, 1, 3), (96, 32, 7, 11), (240, 15, 4, 8)])
+@pytest.mark.parametrize("T", [9, 2070])
+def test_route_groups_of_every_width(T, E, groups, topk, k):
+    """Groups of one lane's experts, of several lanes' and of parts of a lane's;
+    some rows with whole groups excluded, some with equal logits throughout."""
+    l = torch.randn((T, E), generator=gen(E + groups))
+    l[3, : 2 * (E // groups)] = float("-inf")
+    l[5] = 1.0
+    l[7, E // groups - 1 :] = float("-inf")
+    bias = torch.randn(E, generator=gen(E)).mul(0.1)
+    for kw in (dict(), dict(group_top=2), dict(bias=bias, score="sigmoid"), dict(bias=bias, group_top=2)):
+        check_route(l, k, groups=groups, topk_groups=topk, **kw)
