@@ -40,7 +40,9 @@ extern "C" {
  *   ids    int32 [T][k]: the experts of the k largest keys left, largest
  *          first; of equal keys (and equal groups) the lowest index;
  *   weights fp32 [T][k]: their scores, divided by their sum with
- *          W4A16_ROUTE_RENORMALIZE (a sum of 0 gives 0), times scale.
+ *          W4A16_ROUTE_RENORMALIZE (a sum of 0 gives 0), times scale.  They are
+ *          formed in 64 bits: a sigmoid of a logit of -700 still weighs, one
+ *          below -745 is 0.
  * A NaN logit counts as -infinity, +infinity as the largest float.  An expert
  * with a logit of -infinity, or a bias of -infinity or NaN, is never chosen
  * (and adds nothing to its group's value): a slot that no expert is left for

@@ -89,6 +89,29 @@ def test_route_excluded_experts_and_odd_values():
         check_route(rows, 4, score="sigmoid", bias=bias, groups=4, topk_groups=2, group_top=2)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T", [40, 2100])
+def test_route_sigmoid_of_very_negative_logits(T, dt):
+    """Scores far below what 32 bits hold still weigh against each other: whole
+    rows of logits from -85 to -700 (their 64-bit scores are normal numbers),
+    with and without a bias of zeros, which takes the keys' wider form."""
+    E, k = 16, 4
+    low = torch.linspace(-85, -700, T)[:, None]
+    l = (low - torch.rand((T, E), generator=gen(5)) * 5).to(DT[dt])
+    l[0, :4] = torch.tensor([-90.0, -91.0, -95.0, -100.0])
+    l[0, 4:] = -float("inf")
+    zeros = torch.zeros(E)
+    check_route(l, k, score="sigmoid")
+    check_route(l, k, score="sigmoid", renormalize=False, scale=2.5)
+    # (groups judged by their best alone: the logits are the keys there too)
+    check_route(l, k, score="sigmoid", groups=4, topk_groups=2)
+    ids, w = moe.route(l.cuda(), k, score="sigmoid")
+    assert bool(((w.sum(1) - 1).abs() < 1e-5).all())
+    # a bias of zeros: the same weights wherever it leaves the same experts
+    ids0, w0 = moe.route(l.cuda(), k, score="sigmoid", bias=zeros.cuda())
+    assert torch.equal(ids, ids0) and torch.equal(w, w0)
+
+
 def test_route_empty_and_refusals():
     ids, w = moe.route(torch.zeros((0, 8), device="cuda"), 2)
     assert tuple(ids.shape) == (0, 2) and tuple(w.shape) == (0, 2)

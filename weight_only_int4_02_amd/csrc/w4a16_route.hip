@@ -26,7 +26,7 @@ namespace {
 // The k largest are taken one at a time: the maximum over the row's lanes by
 // DPP moves, then the lowest expert that holds it.  A taken or excluded
 // expert's key is -infinity.  The chosen experts' scores are formed anew from
-// their logits at the end, one lane a slot.
+// their logits at the end, one lane a slot, in 64 bits.
 //
 // The kernel is bound by its instructions and their latency, not its bytes
 // (8192 rows of 256 experts, 9 MB: 17 us, most of it the eight selections).  Few
@@ -100,12 +100,13 @@ __device__ __forceinline__ float clean_logit(float x) {
     return x != x ? -INFINITY : fminf(x, 3.402823466e38f);
 }
 
-// exp(x) in 64 bits, without the branches of a library's: x = n ln 2 + r with
-// |r| <= ln 2 / 2 (ln 2 in two parts, so that n times the first is exact), the
-// exponential's series to r^13 / 13! (the next term is below 2^-57), times
-// 2^n.  Below -745 it is 0, above 709 infinite, as the rounded exponential is.
+// exp(x) for x <= 0 in 64 bits, without the branches of a library's.  Cody and
+// Waite's reduction: x = n ln 2 + r with |r| <= ln 2 / 2, ln 2 in two parts, so
+// that n times the first is exact; then the exponential's series to r^13 / 13!
+// (the next term is below 2^-57), times 2^n.  Below -745, where the result
+// would round to less than the smallest subnormal, it is 0.
 __device__ __forceinline__ double exp_series(double arg) {
-    const double x = fmin(fmax(arg, -745.0), 709.0);
+    const double x = fmax(arg, -745.0);
     const double n = __builtin_rint(x * 1.4426950408889634);
     const double r = fma(n, -1.9082149292705877e-10, fma(n, -0.6931471803691238, x));
     double y = 1.0 / 6227020800.0;
@@ -117,28 +118,23 @@ __device__ __forceinline__ double exp_series(double arg) {
     for (int k = 0; k < 13; k++)
         y = fma(y, r, over[k]);
     y = ldexp(y, (int)n);
-    return arg < -745.0 ? 0.0 : arg > 709.0 ? (double)INFINITY : y;
+    return arg < -745.0 ? 0.0 : y;
 }
-// 1 / v for 1 <= v (0 above 1e300), by two steps of Newton's from the
-// hardware's estimate.
+// 1 / v for 1 <= v <= 2, by two steps of Newton's from the hardware's estimate.
 __device__ __forceinline__ double reciprocal(double v) {
     double y = __builtin_amdgcn_rcp(v);
     y = fma(y, fma(-v, y, 1.0), y);
     y = fma(y, fma(-v, y, 1.0), y);
-    return v > 1e300 ? 0.0 : y;
+    return y;
 }
 
-// A logit's score: sigmoid, or softmax's numerator.  -infinity has none.
-template <typename Key>
-__device__ __forceinline__ Key score_of(float l, float top, bool sigmoid) {
-    Key s;
-    if constexpr (sizeof(Key) == 8) {
-        const double e = exp_series(sigmoid ? -(double)l : (double)l - (double)top);
-        s = sigmoid ? reciprocal(1.0 + e) : e;
-    } else {
-        const float e = expf(sigmoid ? -l : l - top);
-        s = sigmoid ? 1.f / (1.f + e) : e;
-    }
+// A logit's score in 64 bits: sigmoid, or softmax's numerator.  The sigmoid is
+// formed from e = exp(-|l|), as 1 / (1 + e) or e / (1 + e), so that nothing
+// overflows and the score of a very negative logit keeps its bits (a row may
+// have no others, and is then divided by their sum).  -infinity has none.
+__device__ __forceinline__ double score_of(float l, float top, bool sigmoid) {
+    const double e = exp_series(sigmoid ? -fabs((double)l) : (double)l - (double)top);
+    const double s = sigmoid ? (l < 0 ? e : 1.0) * reciprocal(1.0 + e) : e;
     return l == -INFINITY ? 0 : s;
 }
 
@@ -195,7 +191,10 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         Key sum = 0;
 #pragma unroll
         for (int v = 0; v < V; v++) {
-            key[v] = score_of<Key>(lg[v], top, sig);
+            if constexpr (WIDE)
+                key[v] = score_of(lg[v], top, sig);
+            else
+                key[v] = lg[v] == -INFINITY ? 0.f : expf(lg[v] - top);
             sum += key[v];
         }
         if (!sig) {
@@ -337,16 +336,18 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
             id[n] = j == l + n * L ? at : id[n];
     }
 
-    Key w[NS], total = 0;
+    // in 64 bits whatever the keys are: a chosen sigmoid may be far below what
+    // 32 bits hold, and one lane a slot costs next to nothing
+    double w[NS], total = 0;
 #pragma unroll
     for (int n = 0; n < NS; n++) {
         const float x =
             id[n] < 0 ? -INFINITY : clean_logit(load_logit(a, base + id[n]));
-        w[n] = score_of<Key>(x, top, sig) * inv;
+        w[n] = score_of(x, top, sig) * inv;
         total += w[n];
     }
     if (a.renormalize) {
-        total = row_reduce<L>(total, [](Key x, Key y) { return x + y; });
+        total = row_reduce<L>(total, [](double x, double y) { return x + y; });
 #pragma unroll
         for (int n = 0; n < NS; n++)
             w[n] = total > 0 ? w[n] / total : 0;
@@ -356,7 +357,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteArgs a) {
         const int j = l + n * L;
         if (t_own < a.T && j < a.k) {
             a.ids[t * a.k + j] = id[n];
-            a.weights[t * a.k + j] = id[n] < 0 ? 0.f : (float)(w[n] * (Key)a.scale);
+            a.weights[t * a.k + j] = id[n] < 0 ? 0.f : (float)(w[n] * (double)a.scale);
         }
     }
 }
