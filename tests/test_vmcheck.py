@@ -9,6 +9,59 @@ def found(body: str):
     return vmcheck.check_asm(asm).get("_Zkern", [])
 
 
+def early(body: str):
+    asm = "_Zkern:\n" + body.strip("\n") + "\n.Lfunc_end0:\n"
+    return vmcheck.check_asm_sgprs(asm).get("_Zkern", [])
+
+
+def test_a_descriptor_reloaded_right_before_its_load_is_reported():
+    # as the compiler reloads scalar registers that it keeps in lanes of a
+    # vector register, and does not see that the inline load reads them
+    body = """
+    v_readlane_b32 s14, v205, 18
+    v_readlane_b32 s15, v205, 19
+    {}
+    ;;#ASMSTART
+    buffer_load_ushort v183, v2, s[12:15], 0 offen
+    ;;#ASMEND
+    s_endpgm
+"""
+    f = early(body.format(""))
+    assert len(f) == 1 and f[0][2] == [("s", 14), ("s", 15)]
+    assert early(body.format("s_nop 3"))[0][2] == [("s", 15)]   # four wait states; s14 has its five
+    assert early(body.format("s_nop 4")) == []
+    # the compiler's own form: one each for the instructions between
+    assert early(body.format("s_nop 1\n    v_mov_b32 v1, v2\n    s_add_i32 s3, s3, 1\n    s_nop 0")) == []
+    # a scalar instruction's write in between takes the register over
+    assert [r for x in early(body.format("s_mov_b32 s15, 0x20000")) for r in x[2]] == [("s", 14)]
+
+
+def test_scalar_wait_states_over_branches_and_other_writers():
+    f = early("""
+    s_cbranch_scc0 .LBB0_2
+    v_readfirstlane_b32 s5, v1
+    s_branch .LBB0_3
+.LBB0_2:
+    s_mov_b32 s5, 0
+.LBB0_3:
+    buffer_load_dwordx4 v[4:7], v1, s[8:11], s5 offen
+    s_endpgm
+""")
+    assert len(f) == 1 and f[0][2] == [("s", 5)]
+    assert early("""
+    v_cmp_eq_u32_e64 s[8:9], v1, v2
+    buffer_load_dword v4, v1, s[8:11], 0 offen
+    s_endpgm
+""")[0][2] == [("s", 8), ("s", 9)]
+    # a scalar operand of a compare is read, not written
+    assert early("""
+    v_cmp_eq_u32_e32 vcc, s5, v2
+    v_mov_b32_e32 v9, s6
+    buffer_load_dword v4, v1, s[8:11], s5 offen
+    s_endpgm
+""") == []
+
+
 def test_read_before_wait_is_reported():
     f = found("""
     buffer_load_dwordx4 v[4:7], v1, s[8:11], 0 offen

@@ -82,7 +82,10 @@ def _check_inflight(src: str) -> None:
     spill, so the remarks above miss it (the compiler has split such live
     ranges into AGPRs under register pressure): the device assembly of the
     same compile is checked against a model of the load counter
-    (vmcheck.py), and any kernel that names such a register fails the build."""
+    (vmcheck.py), and any kernel that names such a register fails the build.
+    So does one whose vector-memory instruction reads a scalar register sooner
+    than five wait states after a vector instruction wrote it: the compiler
+    does not keep that distance for inline assembly."""
     from . import vmcheck
 
     asm = os.path.join(BUILD_DIR, os.path.basename(src) + ".s")
@@ -92,12 +95,14 @@ def _check_inflight(src: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     with open(asm) as f:
-        found = vmcheck.check_asm(f.read())
-    if found:
-        lines = "\n".join(f"  {vmcheck.demangle(k)}: line {v[0][0]} {v[0][1]!r}"
-                          for k, v in found.items())
-        raise RuntimeError(f"{src}: kernels name registers of loads still in flight "
-                           f"({asm}):\n{lines}")
+        text = f.read()
+    for check, what in ((vmcheck.check_asm, "name registers of loads still in flight"),
+                        (vmcheck.check_asm_sgprs, "read scalar registers too soon after a vector write")):
+        found = check(text)
+        if found:
+            lines = "\n".join(f"  {vmcheck.demangle(k)}: line {v[0][0]} {v[0][1]!r}"
+                              for k, v in found.items())
+            raise RuntimeError(f"{src}: kernels {what} ({asm}):\n{lines}")
 
 
 def build_library(verbose: bool = False) -> str:

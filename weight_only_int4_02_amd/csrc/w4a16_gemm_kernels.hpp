@@ -52,14 +52,31 @@ __device__ __forceinline__ i4_t make_desc(const void *base, uint32_t bytes) {
 // registers (reg_fence) so no consumer is scheduled above the wait.  Left to
 // the compiler, the waits on loop-carried prefetch registers are
 // conservative and drain the prefetch pipeline.
+// The compiler does not look into them for hazards either: a vector-memory
+// instruction may read a scalar register no sooner than five wait states after
+// a vector instruction wrote it.  Where a kernel keeps scalar registers in lanes of a
+// vector register (v_readlane_b32 brings them back, right before the load if
+// need be), NOPS puts the five in front of each load; elsewhere no vector
+// instruction writes a load's scalar registers so late, which the build checks
+// for every kernel (vmcheck.py).
+template <bool NOPS = false>
 __device__ __forceinline__ uint32_t load_u16_untracked(i4_t desc, uint32_t voffset) {
     uint32_t v;
-    asm volatile("buffer_load_ushort %0, %1, %2, 0 offen" : "=v"(v) : "v"(voffset), "s"(desc));
+    if constexpr (NOPS)
+        asm volatile("s_nop 4\n\tbuffer_load_ushort %0, %1, %2, 0 offen"
+                     : "=v"(v) : "v"(voffset), "s"(desc));
+    else
+        asm volatile("buffer_load_ushort %0, %1, %2, 0 offen" : "=v"(v) : "v"(voffset), "s"(desc));
     return v;
 }
+template <bool NOPS = false>
 __device__ __forceinline__ uint32_t load_u32_untracked(i4_t desc, uint32_t voffset) {
     uint32_t v;
-    asm volatile("buffer_load_dword %0, %1, %2, 0 offen" : "=v"(v) : "v"(voffset), "s"(desc));
+    if constexpr (NOPS)
+        asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, %2, 0 offen"
+                     : "=v"(v) : "v"(voffset), "s"(desc));
+    else
+        asm volatile("buffer_load_dword %0, %1, %2, 0 offen" : "=v"(v) : "v"(voffset), "s"(desc));
     return v;
 }
 __device__ __forceinline__ u4_t load_b128_untracked(i4_t desc, uint32_t voffset) {

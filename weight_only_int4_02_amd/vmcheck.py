@@ -17,6 +17,15 @@ pending on every path (it reports no hazard that a path-insensitive merge
 would invent, and may miss one that exists on some paths only).  An
 instruction that names a register of a load still pending is reported, the
 next load into that register included.
+
+It also checks the wait states of gfx9 that inline assembly has to keep by
+itself: a vector-memory instruction that reads a scalar register (a buffer
+descriptor, a scalar offset) must come at least five wait states after a vector
+instruction wrote that register.  The compiler keeps them for its own
+instructions and does not look into inline assembly, so a scalar register
+reloaded from a lane of a vector register (v_readlane_b32) right before an
+inline buffer load gives the load its old value: a wrong descriptor, and a
+memory fault.
 """
 from __future__ import annotations
 
@@ -145,8 +154,8 @@ def _step(q: Queue, ins: _Instr, report) -> Queue:
     return q
 
 
-def check_kernel(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
-    """[(line, instruction, pending registers it names)] for one kernel."""
+def _graph(body: Sequence[Tuple[int, str]]):
+    """The kernel's basic blocks and each one's successors."""
     blocks = _blocks(body)
     index = {b[0]: i for i, b in enumerate(blocks) if b[0] is not None}
     succs = []
@@ -155,6 +164,12 @@ def check_kernel(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[R
         if falls and i + 1 < len(blocks):
             s.append(i + 1)
         succs.append(s)
+    return blocks, succs
+
+
+def check_kernel(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
+    """[(line, instruction, pending registers it names)] for one kernel."""
+    blocks, succs = _graph(body)
     entry: List[Optional[Queue]] = [None] * len(blocks)
     if blocks:
         entry[0] = ()
@@ -179,6 +194,81 @@ def check_kernel(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[R
     return found
 
 
+_SREG_RANGE = re.compile(r"^s\[(\d+):(\d+)\]$")
+_SREG_ONE = re.compile(r"^s(\d+)$")
+_VMEM_SGPR_WAIT_STATES = 5
+
+
+def _sregs(tok: str) -> FrozenSet[int]:
+    m = _SREG_RANGE.match(tok)
+    if m:
+        return frozenset(range(int(m.group(1)), int(m.group(2)) + 1))
+    m = _SREG_ONE.match(tok)
+    return frozenset({int(m.group(1))}) if m else frozenset()
+
+
+def _tokens(ins: _Instr) -> List[str]:
+    parts = ins.text.split(None, 1)
+    return [t.strip().split(" ")[0] for t in parts[1].split(",")] if len(parts) > 1 else []
+
+
+def _valu_sgpr_writes(ins: _Instr) -> FrozenSet[int]:
+    """Scalar registers a vector instruction writes: the destination of a lane
+    read or of a compare, and the carry-out of an addition."""
+    if ins.op.startswith(("v_readlane", "v_readfirstlane", "v_cmp")):
+        return _sregs(_tokens(ins)[0])
+    if ins.op.startswith(("v_div_scale", "v_mad_u64", "v_mad_i64")) or (ins.op.startswith("v_") and "_co_" in ins.op):
+        return _sregs(_tokens(ins)[1])
+    return frozenset()
+
+
+def _sgpr_step(state: Dict[int, int], ins: _Instr, report) -> Dict[int, int]:
+    """state: scalar register -> wait states since a vector instruction wrote it
+    (below five)."""
+    if state and _is_vmem(ins.op) and report is not None:
+        early = sorted(r for t in _tokens(ins) for r in _sregs(t) if r in state)
+        if early:
+            report(ins, [("s", r) for r in early])
+    n = int(ins.text.split()[1], 0) + 1 if ins.op == "s_nop" else 1
+    state = {r: k + n for r, k in state.items() if k + n < _VMEM_SGPR_WAIT_STATES}
+    if ins.op.startswith("s_"):
+        tok = _tokens(ins)
+        for r in (_sregs(tok[0]) if tok else ()):
+            state.pop(r, None)
+    for r in _valu_sgpr_writes(ins):
+        state[r] = 0
+    return state
+
+
+def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
+    """[(line, instruction, scalar registers it reads too early)], over every
+    path (the fewest wait states of the paths that merge)."""
+    blocks, succs = _graph(body)
+    entry: List[Optional[Dict[int, int]]] = [None] * len(blocks)
+    if blocks:
+        entry[0] = {}
+    work = [0] if blocks else []
+    while work:
+        i = work.pop()
+        q = dict(entry[i])
+        for ins in blocks[i][1]:
+            q = _sgpr_step(q, ins, None)
+        for j in succs[i]:
+            old = entry[j]
+            new = dict(q) if old is None else {r: min(q.get(r, 9), old.get(r, 9)) for r in q.keys() | old.keys()}
+            if new != old:
+                entry[j] = new
+                work.append(j)
+    found = []
+    for i, blk in enumerate(blocks):
+        q = entry[i]
+        if q is None:
+            continue
+        for ins in blk[1]:
+            q = _sgpr_step(q, ins, lambda ins, regs: found.append((ins.line, ins.text, regs)))
+    return found
+
+
 def kernels(asm: str) -> Dict[str, List[Tuple[int, str]]]:
     """Kernel name -> its (line number, text) lines, from a device assembly file."""
     lines = asm.split("\n")
@@ -200,6 +290,10 @@ def check_asm(asm: str) -> Dict[str, List[Tuple[int, str, List[Reg]]]]:
     return {name: f for name, body in kernels(asm).items() for f in [check_kernel(body)] if f}
 
 
+def check_asm_sgprs(asm: str) -> Dict[str, List[Tuple[int, str, List[Reg]]]]:
+    return {name: f for name, body in kernels(asm).items() for f in [check_kernel_sgprs(body)] if f}
+
+
 def demangle(name: str) -> str:
     try:
         return subprocess.run(["c++filt", name], capture_output=True, text=True).stdout.strip() or name
@@ -212,8 +306,11 @@ if __name__ == "__main__":
 
     bad = 0
     for path in sys.argv[1:]:
-        for name, found in check_asm(open(path).read()).items():
-            bad += 1
-            print(f"{path}: {demangle(name)}: {len(found)} instructions name registers of "
-                  f"loads that may be in flight, first: line {found[0][0]} {found[0][1]!r} {found[0][2][:4]}")
+        text = open(path).read()
+        for check, what in ((check_asm, "name registers of loads that may be in flight"),
+                            (check_asm_sgprs, "read scalar registers too soon after a vector write")):
+            for name, found in check(text).items():
+                bad += 1
+                print(f"{path}: {demangle(name)}: {len(found)} instructions {what}, "
+                      f"first: line {found[0][0]} {found[0][1]!r} {found[0][2][:4]}")
     sys.exit(1 if bad else 0)
