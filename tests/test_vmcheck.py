@@ -62,6 +62,110 @@ def test_scalar_wait_states_over_branches_and_other_writers():
 """) == []
 
 
+def paths(body: str):
+    asm = "_Zkern:\n" + body.strip("\n") + "\n.Lfunc_end0:\n"
+    return vmcheck.check_asm_paths(asm).get("_Zkern", [])
+
+
+LOOP_BEFORE_THE_WAIT = """
+    ;;#ASMSTART
+    buffer_load_dwordx4 v[4:7], v1, s[8:11], 0 offen
+    ;;#ASMEND
+    s_cmp_eq_u32 s4, 0
+    s_cbranch_scc1 .LBB0_3
+.LBB0_1:
+    global_load_dword v20, v[10:11], off
+    global_load_dword v21, v[10:11], off offset:4
+    s_waitcnt vmcnt({})
+    {}
+    s_cmp_lg_u32 s4, s5
+    s_cbranch_scc1 .LBB0_1
+.LBB0_3:
+    ;;#ASMSTART
+    s_waitcnt vmcnt(0)
+    ;;#ASMEND
+    v_add_u32_e32 v6, v4, v9
+    s_endpgm
+"""
+
+
+def test_a_loop_of_other_loads_before_the_wait():
+    # the inline load is in flight over a loop whose length nothing bounds: a
+    # register of it is named on a path that no queue common to all holds
+    use = "v_add_u32_e32 v5, v30, v31"
+    assert found(LOOP_BEFORE_THE_WAIT.format(3, use)) == []
+    # two loads follow it in the first round: vmcnt(2) completes it, vmcnt(3) does not
+    f = paths(LOOP_BEFORE_THE_WAIT.format(3, use))
+    assert [x[2] for x in f] == [[("v", 5)]]
+    assert paths(LOOP_BEFORE_THE_WAIT.format(2, use)) == []
+    assert paths(LOOP_BEFORE_THE_WAIT.format(3, "v_add_u32_e32 v30, v30, v31")) == []
+
+
+def test_a_wait_on_another_path_of_a_ring_counts():
+    # the way round the loop is ruled out by its trip count, which the walk
+    # does not know: past a merge with a path that has waited, nothing
+    assert paths("""
+    ;;#ASMSTART
+    buffer_load_dword v4, v1, s[8:11], 0 offen
+    ;;#ASMEND
+    s_cmp_lt_i32 s4, 1
+    s_cbranch_scc1 .LBB0_2
+    ;;#ASMSTART
+    s_waitcnt vmcnt(0)
+    ;;#ASMEND
+    v_add_u32_e32 v6, v4, v9
+.LBB0_2:
+    v_mov_b32_e32 v4, 0
+    s_endpgm
+""") == []
+
+
+BRANCH_FLAG = """
+    s_cmp_eq_u32 s4, 0
+    s_mov_b64 s[12:13], {first}
+    s_cbranch_scc1 .LBB0_2
+    s_mov_b64 s[12:13], {second}
+    ;;#ASMSTART
+    buffer_load_dword v4, v1, s[8:11], 0 offen
+    ;;#ASMEND
+.LBB0_2:
+    s_and_b64 vcc, exec, s[12:13]
+    s_cbranch_vccz .LBB0_4
+    v_mov_b32_e32 v4, 0
+.LBB0_4:
+    ;;#ASMSTART
+    s_waitcnt vmcnt(0)
+    ;;#ASMEND
+    s_endpgm
+"""
+
+
+def test_branch_flags_keep_paths_apart():
+    # the block that writes v4 is taken only where the load was not issued
+    assert paths(BRANCH_FLAG.format(first=-1, second=0)) == []
+    f = paths(BRANCH_FLAG.format(first=0, second=-1))
+    assert [x[2] for x in f] == [[("v", 4)]]
+
+
+def test_exec_is_zero_only_where_it_was_narrowed():
+    body = """
+    ;;#ASMSTART
+    buffer_load_dword v4, v1, s[8:11], 0 offen
+    ;;#ASMEND
+    {}
+    s_cbranch_execz .LBB0_2
+    ;;#ASMSTART
+    s_waitcnt vmcnt(0)
+    ;;#ASMEND
+    s_endpgm
+.LBB0_2:
+    v_mov_b32_e32 v4, 0
+    s_endpgm
+"""
+    assert paths(body.format("s_mov_b32 s4, 0")) == []
+    assert len(paths(body.format("s_and_saveexec_b64 s[4:5], vcc"))) == 1
+
+
 def test_read_before_wait_is_reported():
     f = found("""
     buffer_load_dwordx4 v[4:7], v1, s[8:11], 0 offen

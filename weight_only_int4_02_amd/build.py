@@ -86,23 +86,16 @@ def _check_inflight(src: str) -> None:
     So does one whose vector-memory instruction reads a scalar register sooner
     than five wait states after a vector instruction wrote it: the compiler
     does not keep that distance for inline assembly."""
-    from . import vmcheck
-
     asm = os.path.join(BUILD_DIR, os.path.basename(src) + ".s")
     cmd = [HIPCC] + COMMON + ["-x", "hip", "--offload-device-only", "-S",
                               os.path.join(CSRC, src), "-o", asm]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-    with open(asm) as f:
-        text = f.read()
-    for check, what in ((vmcheck.check_asm, "name registers of loads still in flight"),
-                        (vmcheck.check_asm_sgprs, "read scalar registers too soon after a vector write")):
-        found = check(text)
-        if found:
-            lines = "\n".join(f"  {vmcheck.demangle(k)}: line {v[0][0]} {v[0][1]!r}"
-                              for k, v in found.items())
-            raise RuntimeError(f"{src}: kernels {what} ({asm}):\n{lines}")
+    # (a process of its own: the sources are checked at the same time)
+    r = subprocess.run([sys.executable, os.path.join(PKG, "vmcheck.py"), asm], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{src}: {r.stdout}{r.stderr}")
 
 
 def build_library(verbose: bool = False) -> str:
