@@ -71,7 +71,9 @@ int32_t w4a16_check_route_args(const void *logits, int32_t logits_dtype, int64_t
  *   Y[t] = sum over j of weights[t][j] * (h . Wdown_e^T)
  * with W = RNE((q - z) * s) in the 16-bit type, as w4a16_dequant has it.  All
  * sums are fp32; h is rounded to the 16-bit type between the products (it
- * feeds 16-bit matrix instructions), Y once.  A slot whose id lies outside
+ * feeds 16-bit matrix instructions), Y once.  An h beyond fp16's range enters
+ * the second product in 32 bits instead: a row that has one takes a path of
+ * plain fp32 sums, which is slow.  A slot whose id lies outside
  * 0..E-1 adds nothing; a row with no other slot is 0.  A row may name an
  * expert twice.
  *   gate_up  gated, [E][2][I][K];   down [E][D][I];   Y [T][D].

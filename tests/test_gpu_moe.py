@@ -247,6 +247,35 @@ def test_experts_all_rows_on_one_expert(T, all_one):
     assert not torch.isfinite(y[9]).any()
 
 
+@pytest.mark.parametrize("T,E,k,K,I,D,g,symmetric", [
+    (1, 4, 2, 256, 264, 100, 128, False), (1, 3, 3, 520, 136, 257, 32, True),      # one token
+    (5, 4, 2, 256, 136, 130, 64, False), (50, 2, 1, 264, 200, 64, 128, True),      # direct
+    (90, 8, 2, 256, 136, 257, 32, False),                                          # planned 16-row tiles
+    (150, 6, 2, 392, 264, 260, 64, False), (300, 4, 2, 256, 136, 520, 128, True)]) # 64- and 128-row tiles
+def test_experts_beyond_fp16_on_the_way(T, E, k, K, I, D, g, symmetric):
+    """fp16: silu(gate) up far beyond 65504 that the down projection brings back
+    into range, in some columns of every row, beside rows without any."""
+    case = draw(T, E, k, K, I, D, g, "f16", symmetric, seed=T + I, empty=0.1 if T > 1 else 0.0)
+    X, ids, w, gu, dn = case
+    gu = (gu[0], (gu[1].double() * 300).half(), gu[2])
+    dn = (dn[0], (dn[1].double() * 2.0 ** -7).half(), dn[2])
+    X[3::4] = (X[3::4].double() / 64).half()         # rows that stay in range
+    w[:, 0] = torch.where(torch.arange(T) % 3 == 0, 0.0, w[:, 0])    # a slot of no weight beside them
+    h_max = (X[0].double() @ ref.weight(*[t if t is None else t[int(ids[0, -1])] for t in gu], g).T).abs().max() ** 2
+    assert h_max > 2 * 65504
+    y = check_experts((X, ids, w, gu, dn), g)
+    assert torch.isfinite(y).all()
+    # an infinity in one row of X stays in that row
+    if T > 1:
+        X[4, 7] = float("inf")
+        ids[4] = torch.arange(k)
+        y = moe.experts(*on_gpu((X, ids, w, gu, dn), g)).cpu()
+        fine = torch.arange(T) != 4
+        want, bound = ref.experts(X[fine], ids[fine], w[fine], gu, dn, g)
+        assert bool(((y[fine].double() - want).abs() <= bound).all())
+        assert not torch.isfinite(y[4]).any()
+
+
 def test_experts_is_repeatable_and_keeps_its_neighbours():
     """The same bits each time, into a caller's output and workspace, and
     nothing written before or behind them."""

@@ -126,4 +126,82 @@ __device__ __forceinline__ h8_t mfma8_dequant_bf16_fma(f4_t &c0, f4_t &c1, f4_t 
 #undef W4E_BLOCK
 #undef W4E_M
 
+// ---------------------------------------------------------------------------
+// h = silu(gate) up beyond 65504 does not fit the fp16 operand of the second
+// product: it is stored as infinity, and every result of that row comes out
+// infinite or NaN.  Whoever rounds the results sees that and forms them again
+// here, with each infinite h in 32 bits (from its two rows of the first
+// product) and plain fp32 sums.  Rows without such a value cost a test of
+// their results; one with them is slow (2 K products for each of them).
+// A scale for each row instead would have to be known before the first column
+// of h is stored, and the row's columns are formed by different workgroups.
+// ---------------------------------------------------------------------------
+
+// The columns 8 q .. 8 q + 7 of a weight row; tile0: the matrix's first tile.
+__device__ __forceinline__ h8_t weight8(const ExpertsArgs &a, int64_t tile0, int row, int q) {
+    const int64_t tile = tile0 + (row >> 4);
+    const int r = row & 15, grp = (8 * q) >> a.lg;
+    const uint32_t word = ((const uint32_t *)a.qd)[((tile * a.KT + (q >> 4)) * 64 + r + 16 * (q & 3)) * 4 +
+                                                   ((q >> 2) & 3)];
+    const uint32_t sbits = ((const uint16_t *)a.sd)[(tile * a.G + grp) * 16 + r];
+    const uint32_t z =
+        a.sym ? 8u : (((const uint32_t *)a.zd)[(tile * a.GW + (grp >> 3)) * 16 + r] >> (4 * (grp & 7))) & 0xFu;
+    return dequant_word(word, zero_pair(z), scale_pair(sbits));
+}
+
+// Column i of h for row t of X and expert e, in 32 bits; the whole wave together.
+__device__ __forceinline__ float wide_h(const ExpertsArgs &gu, int64_t t, int e, int i, int lane) {
+    const int64_t gate0 = 2 * (int64_t)e * gu.NT;
+    float g = 0.f, u = 0.f;
+#pragma nounroll
+    for (int q = lane; 8 * q < gu.K; q += 64) {
+        const h8_t x = *(const h8_t *)(gu.X + t * gu.K + 8 * q);
+        const h8_t wg = weight8(gu, gate0, i, q), wu = weight8(gu, gate0 + gu.NT, i, q);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            g = fmaf((float)x[k], (float)wg[k], g);
+            u = fmaf((float)x[k], (float)wu[k], u);
+        }
+    }
+#pragma nounroll
+    for (int d = 1; d < 64; d *= 2) {
+        g += __shfl_xor(g, d);
+        u += __shfl_xor(u, d);
+    }
+    return silu(g) * u;
+}
+
+// h . Wdown for column n (each lane its own), h being row `row` of the stored
+// ones; the whole wave together.
+__device__ __forceinline__ float wide_dot(const ExpertsArgs &gu, const ExpertsArgs &dn, int64_t t, int64_t row,
+                                          int e, int n, int lane) {
+    float out = 0.f;
+#pragma nounroll
+    for (int q = 0; 8 * q < dn.K; q++) {
+        const h8_t stored = *(const h8_t *)(dn.X + row * dn.K + 8 * q);
+        float h[8];
+        uint32_t beyond = 0;   // (the same for all lanes)
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            h[k] = (float)stored[k];
+            beyond |= __builtin_isinf(h[k]) ? 1u << k : 0u;
+        }
+        beyond = __builtin_amdgcn_readfirstlane(beyond);
+#pragma nounroll
+        for (; beyond; beyond &= beyond - 1) {
+            const int at = __builtin_ctz(beyond);
+            const float v = wide_h(gu, t, e, 8 * q + at, lane);
+#pragma unroll
+            for (int k = 0; k < 8; k++)
+                h[k] = k == at ? v : h[k];
+        }
+        asm volatile("" : "+v"(n));   // (its addresses are formed anew, not held over the loop)
+        const h8_t w = weight8(dn, (int64_t)e * dn.NT, n, q);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            out = fmaf(h[k], (float)w[k], out);
+    }
+    return out;
+}
+
 }  // namespace w4a16

@@ -5,6 +5,7 @@
 
 #include <math.h>
 
+#include "w4a16_experts.hpp"
 #include "w4a16_kernels.hpp"
 #include "w4a16_routed.h"
 #include "w4a16_routed.hpp"
@@ -472,72 +473,121 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(
 // slot order; slots without an expert have no row of P.  Four
 // columns per thread where D is a multiple of 4.
 // ---------------------------------------------------------------------------
+// Columns d .. d + C - 1 of row t, stored where `in`; the whole wave together.
+// The kernel's arguments are read again from their own memory, behind a pointer
+// that the compiler knows nothing about: in registers from the start they would
+// cost the kernel half its waves.
+template <int C>
+__device__ __forceinline__ void combine_wide(int64_t t, int64_t d, bool in) {
+    uint64_t args = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(args));
+    const CombineArgs &a = *(const CombineArgs *)(const __attribute__((address_space(4))) CombineArgs *)args;
+#pragma nounroll
+    for (int c = 0; c < C; c++) {
+        float sum = 0.f;
+#pragma nounroll
+        for (int j = 0; j < a.k; j++) {
+            const int64_t s = t * a.k + j;
+            const int id = __builtin_amdgcn_readfirstlane(a.ids[s]);
+            if (id < 0 || id >= a.E)
+                continue;
+            const int64_t row = a.place ? (int64_t)__builtin_amdgcn_readfirstlane(a.place[s]) : s;
+            float p = a.P[row * a.D + d + c];
+            if (__any(!__builtin_isfinite(p)))
+                p = wide_dot(a.gu, a.dn, t, row, id, (int)d + c, threadIdx.x & 63);
+            sum += a.weights[s] * p;
+        }
+        if (in)
+            a.Y[t * a.D + d + c] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+    }
+}
+
 // Columns are cut into blocks of 256 C; a workgroup takes one block of a row.
+constexpr int kCombineRows = 32768;   // rows along a grid's y, at most
 template <bool BF, int C>
 __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
-    const int64_t d = ((int64_t)blockIdx.x * 256 + threadIdx.x) * C;
-    if (d >= a.D)
+    // (threads past the last column form the first ones again and store nothing:
+    // every lane stays active for wide_dot)
+    const int64_t d_own = ((int64_t)blockIdx.x * 256 + threadIdx.x) * C;
+    const int64_t d = d_own < a.D ? d_own : 0;
+    // (one row a workgroup: a loop over rows would hold the arguments in registers
+    // over the rare path below)
+    const int64_t t = (int64_t)blockIdx.z * kCombineRows + blockIdx.y;
+    if (t >= a.T)
         return;
-    for (int64_t t = blockIdx.y; t < a.T; t += gridDim.y) {
-        float acc[C];
+    float acc[C];
 #pragma unroll
-        for (int c = 0; c < C; c++)
-            acc[c] = 0.f;
-        // (the slots' numbers are the same for the whole workgroup)
-        constexpr int U = 4;   // slots whose loads are in flight together
-        for (int j0 = 0; j0 < a.k; j0 += U) {
-            float w[U], v[U][C];
-            bool in[U];
+    for (int c = 0; c < C; c++)
+        acc[c] = 0.f;
+    // (the slots' numbers are the same for the whole workgroup)
+    constexpr int U = 4;   // slots whose loads are in flight together
+    for (int j0 = 0; j0 < a.k; j0 += U) {
+        float w[U], v[U][C];
+        bool in[U];
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int64_t s = t * a.k + j0 + u;
-                in[u] = j0 + u < a.k;
-                const int id = in[u] ? a.ids[s] : -1;
-                in[u] = id >= 0 && id < a.E;
-                if (in[u]) {
-                    w[u] = a.weights[s];
-                    const float *p = a.P + (a.place ? (int64_t)a.place[s] : s) * a.D + d;
-                    if constexpr (C == 4) {
-                        const f4_t x = *(const f4_t *)p;
-#pragma unroll
-                        for (int c = 0; c < C; c++)
-                            v[u][c] = x[c];
-                    } else {
-                        v[u][0] = *p;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; u++)
-                if (in[u]) {
+        for (int u = 0; u < U; u++) {
+            const int64_t s = t * a.k + j0 + u;
+            in[u] = j0 + u < a.k;
+            const int id = in[u] ? a.ids[s] : -1;
+            in[u] = id >= 0 && id < a.E;
+            if (in[u]) {
+                w[u] = a.weights[s];
+                const float *p = a.P + (a.place ? (int64_t)a.place[s] : s) * a.D + d;
+                if constexpr (C == 4) {
+                    const f4_t x = *(const f4_t *)p;
 #pragma unroll
                     for (int c = 0; c < C; c++)
-                        acc[c] += w[u] * v[u][c];
+                        v[u][c] = x[c];
+                } else {
+                    v[u][0] = *p;
                 }
+            }
         }
-        uint16_t out[C];
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            if constexpr (BF)
-                out[c] = __builtin_bit_cast(uint16_t, (__bf16)acc[c]);
-            else
-                out[c] = __builtin_bit_cast(uint16_t, (_Float16)acc[c]);
+        for (int u = 0; u < U; u++)
+            if (in[u]) {
+#pragma unroll
+                for (int c = 0; c < C; c++)
+                    acc[c] += w[u] * v[u][c];
+            }
+    }
+    if constexpr (!BF) {
+        bool finite = true;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+            finite = finite && __builtin_isfinite(acc[c]);
+        if (__builtin_expect(__any(!finite), 0)) {
+            // an h beyond fp16 in one of the slots (or a routing weight, X
+            // or W that is not finite): the wave's columns again, one by
+            // one, with such slots' h in 32 bits
+            combine_wide<C>(t, d, d_own < a.D);
+            return;
         }
-        uint16_t *y = a.Y + t * a.D + d;
-        if constexpr (C == 4) {
-            typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
-            *(u2_t *)y = u2_t{out[0] | (uint32_t)out[1] << 16, out[2] | (uint32_t)out[3] << 16};
-        } else {
-            y[0] = out[0];
-        }
+    }
+    if (d_own >= a.D)
+        return;
+    uint16_t out[C];
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+        if constexpr (BF)
+            out[c] = __builtin_bit_cast(uint16_t, (__bf16)acc[c]);
+        else
+            out[c] = __builtin_bit_cast(uint16_t, (_Float16)acc[c]);
+    }
+    uint16_t *y = a.Y + t * a.D + d;
+    if constexpr (C == 4) {
+        typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+        *(u2_t *)y = u2_t{out[0] | (uint32_t)out[1] << 16, out[2] | (uint32_t)out[3] << 16};
+    } else {
+        y[0] = out[0];
     }
 }
 
 template <bool BF>
 void launch_combine(const CombineArgs &a, hipStream_t st) {
     const int c = (a.D & 3) == 0 ? 4 : 1;
-    const dim3 grid((unsigned)((a.D + 256 * c - 1) / (256 * c)),
-                    (unsigned)(a.T < 32768 ? a.T : 32768));
+    const unsigned rows = (unsigned)(a.T < kCombineRows ? a.T : kCombineRows);
+    const dim3 grid((unsigned)((a.D + 256 * c - 1) / (256 * c)), rows, (unsigned)((a.T + rows - 1) / rows));
     if (c == 4)
         hipLaunchKernelGGL((experts_combine_kernel<BF, 4>), grid, dim3(256), 0, st, a);
     else

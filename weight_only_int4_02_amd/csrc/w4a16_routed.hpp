@@ -72,6 +72,7 @@ struct CombineArgs {
     uint16_t *Y;            // [T][D]
     int64_t T, D;
     int k, E, bf16;
+    ExpertsArgs gu, dn;     // the two products (fp16: rows whose h overflowed)
 };
 
 int launch_expert_plan(const int32_t *ids, int R, int E, int bm, int tiles_max, ExpertTile *tiles,
@@ -80,8 +81,11 @@ int launch_experts_small(const ExpertsArgs &a, const ExpertsPlan &p, bool gated,
 int launch_experts_small_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_large(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
 int launch_experts_large_bf16(const ExpertsArgs &a, const ExpertsPlan &p, bool gated, void *stream);
-int launch_experts_one(const ExpertsArgs &a, const float *weights, bool gated, void *stream);
-int launch_experts_one_bf16(const ExpertsArgs &a, const float *weights, bool gated, void *stream);
+// (gu: the first product, whichever is launched)
+int launch_experts_one(const ExpertsArgs &a, const ExpertsArgs &gu, const float *weights, bool gated,
+                       void *stream);
+int launch_experts_one_bf16(const ExpertsArgs &a, const ExpertsArgs &gu, const float *weights, bool gated,
+                            void *stream);
 int launch_experts_combine(const CombineArgs &a, void *stream);
 
 // ---- adapters ----------------------------------------------------------------

@@ -109,9 +109,9 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
     if (p.one) {
         const auto one = bf ? launch_experts_one_bf16 : launch_experts_one;
         dn.Y = Y;
-        e = one(gu, weights, true, stream);
+        e = one(gu, gu, weights, true, stream);
         if (!e)
-            e = one(dn, weights, false, stream);
+            e = one(dn, gu, weights, false, stream);
         return finish_launch("w4a16_experts", e);
     }
     const auto launch = p.large ? (bf ? launch_experts_large_bf16 : launch_experts_large)
@@ -132,6 +132,8 @@ int32_t w4a16_experts(const uint16_t *X, int64_t T, int64_t K, const int32_t *id
         c.k = k;
         c.E = (int)E;
         c.bf16 = bf ? 1 : 0;
+        c.gu = gu;
+        c.dn = dn;
         e = launch_experts_combine(c, stream);
     }
     return finish_launch("w4a16_experts", e);

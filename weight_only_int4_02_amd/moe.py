@@ -239,7 +239,8 @@ def experts(X: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor, gate_up: 
 
     X [T, K] fp16 or bf16 (the weights' format), ids int32 [T, k] and weights
     fp32 [T, k] as route() gives them.  A slot with an id outside 0..E-1 adds
-    nothing; a row with no other slot is 0.  T may be 0.
+    nothing; a row with no other slot is 0.  T may be 0.  fp16: a row whose h
+    leaves the type's range somewhere is still right, but slow.
 
     workspace: at least experts_workspace_size() bytes, for callers that
     manage their own; without one, each call takes a new block of torch's
