@@ -140,3 +140,23 @@ def test_binding_refuses_what_it_cannot_take():
         moe.expert_weight(torch.zeros((2, 8, 32), dtype=torch.uint8), torch.zeros((2, 8, 1), dtype=torch.float16), None, 32)
     with pytest.raises(TypeError):
         lora.adapters(torch.zeros((2, 8, 32)), torch.zeros((2, 8, 8)), torch.zeros(2, dtype=f))
+
+
+def test_a_layers_rows_and_logits_belong_together():
+    """Shapes that only hold as many elements are refused before any call: rows
+    would meet other rows' logits or adapters."""
+    from weight_only_int4_02_amd.qlinear import QLinear
+
+    def weight(N, K, gated):
+        return moe.ExpertWeight(torch.zeros(0), torch.zeros(0), None, 4, N, K, 32, w4.SYMMETRIC, gated)
+
+    layer = moe.QExperts(weight(32, 64, True), weight(64, 32, False), k=2)
+    for x, logits in (((4, 64), (2, 8)), ((2, 128), (4, 4)), ((2, 3, 64), (3, 2, 4)), ((2, 3, 64), (6, 4)), ((6, 64), (24,))):
+        with pytest.raises(ValueError, match="logits"):
+            layer(torch.zeros(x, dtype=torch.float16), torch.zeros(logits))
+    q = QLinear.__new__(QLinear)
+    torch.nn.Module.__init__(q)
+    q.K, q.N, q.bias, q.packed = 64, 32, None, None
+    for x, ids in (((2, 3, 64), (3, 2)), ((2, 3, 64), (1, 6)), ((2, 3, 64), (2, 4)), ((6, 64), (5,))):
+        with pytest.raises(ValueError, match="ids"):
+            q(torch.zeros(x, dtype=torch.float16), adapters=object(), ids=torch.zeros(ids, dtype=torch.int32))

@@ -300,6 +300,10 @@ class QExperts(torch.nn.Module):
 
     def forward(self, x: torch.Tensor, logits: torch.Tensor,
                 out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        if (x.shape[:-1] != logits.shape[:-1] or x.shape[-1:] != (self.gate_up.K,)
+                or logits.shape[-1:] != (self.gate_up.E,)):
+            raise ValueError(f"x must be [..., {self.gate_up.K}] and logits [..., {self.gate_up.E}] with the "
+                             f"same leading dimensions, got {tuple(x.shape)} and {tuple(logits.shape)}")
         ids, weights = route(logits.reshape(-1, self.gate_up.E), **self.routing)
         y = experts(x.reshape(-1, self.gate_up.K), ids, weights, self.gate_up, self.down, out=out)
         return y.reshape(*x.shape[:-1], self.down.N)

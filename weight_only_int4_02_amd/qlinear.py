@@ -63,10 +63,13 @@ class QLinear(torch.nn.Module):
                 adapters: Optional[Adapters] = None,
                 ids: Optional[torch.Tensor] = None) -> torch.Tensor:
         """adapters, ids: low-rank adapters and the adapter of each row of x
-        (int32, x's leading dimensions; -1 for none), added by gemm_lora."""
+        (int32, x's leading dimensions or its rows in one; -1 for none), added by
+        gemm_lora."""
         shape = x.shape
         if (adapters is None) != (ids is None):
             raise ValueError("adapters and ids go together")
+        if ids is not None and ids.shape != shape[:-1] and ids.shape != (shape[:-1].numel(),):
+            raise ValueError(f"ids must have x's leading dimensions {tuple(shape[:-1])}, or be one number a row")
         if adapters is None:
             y = gemm(x.reshape(-1, self.K), self.packed, out=out)
         else:
