@@ -132,76 +132,131 @@ __device__ __forceinline__ h8_t mfma8_dequant_bf16_fma(f4_t &c0, f4_t &c1, f4_t 
 // infinite or NaN.  Whoever rounds the results sees that and forms them again
 // here, with each infinite h in 32 bits (from its two rows of the first
 // product) and plain fp32 sums.  Rows without such a value cost a test of
-// their results; one with them is slow (2 K products for each of them).
-// A scale for each row instead would have to be known before the first column
-// of h is stored, and the row's columns are formed by different workgroups.
+// their results.  One token through two experts of the 7B MLP's size, 34 us,
+// takes 0.8 ms with a few such columns and 20 ms with a sixth of them; 4096
+// tokens over 64 experts with one such row 1.2 and 7 ms instead of 0.5.  A
+// scale for each row instead would have to be known before the first column of
+// h is stored, and the row's columns are formed by different workgroups.
 // ---------------------------------------------------------------------------
 
-// The columns 8 q .. 8 q + 7 of a weight row; tile0: the matrix's first tile.
-__device__ __forceinline__ h8_t weight8(const ExpertsArgs &a, int64_t tile0, int row, int q) {
-    const int64_t tile = tile0 + (row >> 4);
-    const int r = row & 15, grp = (8 * q) >> a.lg;
-    const uint32_t word = ((const uint32_t *)a.qd)[((tile * a.KT + (q >> 4)) * 64 + r + 16 * (q & 3)) * 4 +
-                                                   ((q >> 2) & 3)];
-    const uint32_t sbits = ((const uint16_t *)a.sd)[(tile * a.G + grp) * 16 + r];
-    const uint32_t z =
-        a.sym ? 8u : (((const uint32_t *)a.zd)[(tile * a.GW + (grp >> 3)) * 16 + r] >> (4 * (grp & 7))) & 0xFu;
-    return dequant_word(word, zero_pair(z), scale_pair(sbits));
+// One expert's matrices (uniform), addressed by 32-bit offsets from their first
+// tile, and the scale bits and zero of the group of columns 8 q .. of row r of a
+// tile.
+struct ExpertBase {
+    const uint32_t *q, *z;
+    const uint16_t *s;
+};
+__device__ __forceinline__ ExpertBase expert_base(const ExpertsArgs &a, int e, int parts) {
+    const int64_t tile = (int64_t)e * parts * a.NT;
+    return {(const uint32_t *)a.qd + tile * a.KT * 256, a.sym ? nullptr : (const uint32_t *)a.zd + tile * a.GW * 16,
+            (const uint16_t *)a.sd + tile * a.G * 16};
+}
+struct RowGroup {
+    uint32_t s, z;
+};
+__device__ __forceinline__ RowGroup row_group(const ExpertsArgs &a, const ExpertBase &b, uint32_t tile, uint32_t r,
+                                              int q) {
+    const uint32_t grp = (uint32_t)min((8 * q) >> a.lg, a.G - 1);
+    const uint32_t s = b.s[(tile * a.G + grp) * 16 + r];
+    const uint32_t z = a.sym ? 8u : (b.z[(tile * a.GW + (grp >> 3)) * 16 + r] >> (4 * (grp & 7))) & 0xFu;
+    return {s, z};
 }
 
 // Column i of h for row t of X and expert e, in 32 bits; the whole wave together.
 __device__ __forceinline__ float wide_h(const ExpertsArgs &gu, int64_t t, int e, int i, int lane) {
-    const int64_t gate0 = 2 * (int64_t)e * gu.NT;
-    float g = 0.f, u = 0.f;
-#pragma nounroll
+    const ExpertBase b = expert_base(gu, e, 2);
+    const uint32_t tile = (uint32_t)i >> 4, r = i & 15;   // (up's: NT further)
+    const uint16_t *x_row = gu.X + t * gu.K;
+    float sum[2] = {0.f, 0.f};
     for (int q = lane; 8 * q < gu.K; q += 64) {
-        const h8_t x = *(const h8_t *)(gu.X + t * gu.K + 8 * q);
-        const h8_t wg = weight8(gu, gate0, i, q), wu = weight8(gu, gate0 + gu.NT, i, q);
+        const h8_t x = *(const h8_t *)(x_row + 8 * q);
 #pragma unroll
-        for (int k = 0; k < 8; k++) {
-            g = fmaf((float)x[k], (float)wg[k], g);
-            u = fmaf((float)x[k], (float)wu[k], u);
-        }
-    }
-#pragma nounroll
-    for (int d = 1; d < 64; d *= 2) {
-        g += __shfl_xor(g, d);
-        u += __shfl_xor(u, d);
-    }
-    return silu(g) * u;
-}
-
-// h . Wdown for column n (each lane its own), h being row `row` of the stored
-// ones; the whole wave together.
-__device__ __forceinline__ float wide_dot(const ExpertsArgs &gu, const ExpertsArgs &dn, int64_t t, int64_t row,
-                                          int e, int n, int lane) {
-    float out = 0.f;
-#pragma nounroll
-    for (int q = 0; 8 * q < dn.K; q++) {
-        const h8_t stored = *(const h8_t *)(dn.X + row * dn.K + 8 * q);
-        float h[8];
-        uint32_t beyond = 0;   // (the same for all lanes)
-#pragma unroll
-        for (int k = 0; k < 8; k++) {
-            h[k] = (float)stored[k];
-            beyond |= __builtin_isinf(h[k]) ? 1u << k : 0u;
-        }
-        beyond = __builtin_amdgcn_readfirstlane(beyond);
-#pragma nounroll
-        for (; beyond; beyond &= beyond - 1) {
-            const int at = __builtin_ctz(beyond);
-            const float v = wide_h(gu, t, e, 8 * q + at, lane);
+        for (int p = 0; p < 2; p++) {
+            const uint32_t tp = tile + p * gu.NT;
+            const RowGroup g = row_group(gu, b, tp, r, q);
+            const uint32_t word = b.q[((tp * gu.KT + (q >> 4)) * 64 + r + 16 * (q & 3)) * 4 + ((q >> 2) & 3)];
+            const h8_t w = dequant_word(word, zero_pair(g.z), scale_pair(g.s));
 #pragma unroll
             for (int k = 0; k < 8; k++)
-                h[k] = k == at ? v : h[k];
+                sum[p] = fmaf((float)x[k], (float)w[k], sum[p]);
         }
-        asm volatile("" : "+v"(n));   // (its addresses are formed anew, not held over the loop)
-        const h8_t w = weight8(dn, (int64_t)e * dn.NT, n, q);
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            out = fmaf(h[k], (float)w[k], out);
     }
-    return out;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        sum[0] += __shfl_xor(sum[0], d);
+        sum[1] += __shfl_xor(sum[1], d);
+    }
+    return silu(sum[0]) * sum[1];
+}
+
+// Columns of h that a wave holds in LDS at once, in 32 bits.
+constexpr int kWideColumns = 1024;
+
+// out += weight h . Wdown for columns n .. n + C - 1 (each lane its own n), h being
+// row `row` of the stored ones; the whole wave together, hs its own LDS.
+template <int C>
+__device__ __forceinline__ void wide_dot(const ExpertsArgs &gu, const ExpertsArgs &dn, int64_t t, int64_t row,
+                                         int e, float weight, int n, int lane, float *hs, float (&out)[C]) {
+    const ExpertBase b = expert_base(dn, e, 1);
+#pragma nounroll
+    for (int i0 = 0; i0 < dn.K; i0 += kWideColumns) {
+#pragma nounroll
+        for (int at = 8 * lane; at < kWideColumns; at += 512) {
+            h8_t stored = {};
+            if (i0 + at < dn.K)
+                stored = *(const h8_t *)(dn.X + row * dn.K + i0 + at);
+            uint32_t inf = 0;
+#pragma unroll
+            for (int k = 0; k < 8; k++) {
+                hs[at + k] = (float)stored[k];
+                inf |= __builtin_isinf((float)stored[k]) ? 1u << k : 0u;
+            }
+            // one by one, the whole wave on each
+            for (uint64_t lanes = __ballot(inf != 0); lanes; lanes &= lanes - 1) {
+                const int from = __builtin_ctzll(lanes);
+                const int base = at - 8 * lane + 8 * from;
+                for (uint32_t bits = __builtin_amdgcn_readlane(inf, from); bits; bits &= bits - 1) {
+                    const int i = base + __builtin_ctz(bits);
+                    const float v = wide_h(gu, t, e, __builtin_amdgcn_readfirstlane(i0 + i), lane);
+                    if (lane == from)
+                        hs[i] = v;
+                }
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int kt1 = min(dn.KT, (i0 + kWideColumns) >> 7);
+#pragma nounroll
+        for (int kt = i0 >> 7; kt < kt1; kt++) {
+#pragma nounroll
+            for (int c = 0; c < C; c++) {
+                const uint32_t tile = (uint32_t)(n + c) >> 4, r = (n + c) & 15;
+                float part = 0.f;
+#pragma nounroll
+                for (int i = 0; i < 4; i++) {
+                    const u4_t word = ((const u4_t *)b.q)[(tile * dn.KT + kt) * 64 + r + 16 * i];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        // (a word at a time: the next one's values only after this
+                        // one's sum, or they would take all registers)
+                        uint32_t at = (uint32_t)(kt * 128 - i0 + 32 * j + 8 * i), wd = word[j];
+                        asm volatile("" : "+v"(at), "+v"(wd), "+v"(part));
+                        const RowGroup g = row_group(dn, b, tile, r, 16 * kt + 4 * j);
+                        const h8_t w = dequant_word(wd, zero_pair(g.z), scale_pair(g.s));
+                        const f4_t h0 = *(const f4_t *)&hs[at], h1 = *(const f4_t *)&hs[at + 4];
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            part = fmaf(h0[k], (float)w[k], part);
+                            part = fmaf(h1[k], (float)w[4 + k], part);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < C; k++)
+                    out[k] += k == c ? weight * part : 0.f;
+            }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // (before the next columns)
+    }
 }
 
 }  // namespace w4a16

@@ -473,33 +473,48 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(
 // slot order; slots without an expert have no row of P.  Four
 // columns per thread where D is a multiple of 4.
 // ---------------------------------------------------------------------------
-// Columns d .. d + C - 1 of row t, stored where `in`; the whole wave together.
+// Columns d .. d + C - 1 of row t once more, where an h beyond fp16 (or a routing
+// weight, X or W that is not finite) left one without a finite sum: the slots
+// whose results are not finite with h in 32 bits.  Stored where `in`; the whole
+// wave together.
 // The kernel's arguments are read again from their own memory, behind a pointer
 // that the compiler knows nothing about: in registers from the start they would
-// cost the kernel half its waves.
+// cost the kernel waves.
 template <int C>
 __device__ __forceinline__ void combine_wide(int64_t t, int64_t d, bool in) {
     uint64_t args = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(args));
     const CombineArgs &a = *(const CombineArgs *)(const __attribute__((address_space(4))) CombineArgs *)args;
+    __shared__ __align__(16) float hs[4][kWideColumns];
+    const int lane = threadIdx.x & 63;
+    float sum[C];
+#pragma unroll
+    for (int c = 0; c < C; c++)
+        sum[c] = 0.f;
 #pragma nounroll
-    for (int c = 0; c < C; c++) {
-        float sum = 0.f;
-#pragma nounroll
-        for (int j = 0; j < a.k; j++) {
-            const int64_t s = t * a.k + j;
-            const int id = __builtin_amdgcn_readfirstlane(a.ids[s]);
-            if (id < 0 || id >= a.E)
-                continue;
-            const int64_t row = a.place ? (int64_t)__builtin_amdgcn_readfirstlane(a.place[s]) : s;
-            float p = a.P[row * a.D + d + c];
-            if (__any(!__builtin_isfinite(p)))
-                p = wide_dot(a.gu, a.dn, t, row, id, (int)d + c, threadIdx.x & 63);
-            sum += a.weights[s] * p;
-        }
-        if (in)
-            a.Y[t * a.D + d + c] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+    for (int j = 0; j < a.k; j++) {
+        const int64_t s = t * a.k + j;
+        const int id = __builtin_amdgcn_readfirstlane(a.ids[s]);
+        if (id < 0 || id >= a.E)
+            continue;
+        const int64_t row = a.place ? (int64_t)__builtin_amdgcn_readfirstlane(a.place[s]) : s;
+        const float weight = a.weights[s];
+        const float *p = a.P + row * a.D + d;
+        bool whole = true;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+            whole = whole && __builtin_isfinite(p[c]);
+        if (__any(!whole))
+            wide_dot<C>(a.gu, a.dn, t, row, id, weight, (int)d, lane, hs[threadIdx.x >> 6], sum);
+        else
+#pragma unroll
+            for (int c = 0; c < C; c++)
+                sum[c] += weight * p[c];
     }
+#pragma unroll
+    for (int c = 0; c < C; c++)
+        if (in)
+            a.Y[t * a.D + d + c] = __builtin_bit_cast(uint16_t, (_Float16)sum[c]);
 }
 
 // Columns are cut into blocks of 256 C; a workgroup takes one block of a row.
@@ -557,9 +572,6 @@ __global__ __launch_bounds__(256) void experts_combine_kernel(CombineArgs a) {
         for (int c = 0; c < C; c++)
             finite = finite && __builtin_isfinite(acc[c]);
         if (__builtin_expect(__any(!finite), 0)) {
-            // an h beyond fp16 in one of the slots (or a routing weight, X
-            // or W that is not finite): the wave's columns again, one by
-            // one, with such slots' h in 32 bits
             combine_wide<C>(t, d, d_own < a.D);
             return;
         }
