@@ -6,9 +6,11 @@
 namespace w4a16 {
 
 // v / (1 + exp(-v)).  exp2 and the reciprocal by the hardware's instructions,
-// each good to one step of 32 bits; the product v log2(e) before the exp2 is
-// rounded too, so the result is off by at most (2 |v| + 4) 2^-24 of itself --
-// nothing beside the rounding of h to 16 bits.  exp(-v) overflowing gives -0.
+// each good to one step of 32 bits (2 units of 2^-24); log2(e) and its product
+// with v are rounded before the exp2 (2 |v| units), the sum and the last product
+// after it (one each): off by at most (2 |v| + 8) 2^-24 of itself down to v = -87
+// -- nothing beside the rounding of h to 16 bits.  Below, where it is less than
+// 2^-119, the reciprocal's result is subnormal and may be flushed: -0.
 __device__ __forceinline__ float silu(float v) {
     return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504088896341f * v));
 }

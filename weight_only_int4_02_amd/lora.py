@@ -116,7 +116,8 @@ def gemm_lora(X: torch.Tensor, w: PackedWeight, ad: Adapters, ids: torch.Tensor,
               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """gemm() with an adapter for each row: Y [M, N] as above, X [M, K] fp16 or
     bf16 (the weight's and the adapters' format), ids int32 [M].  A row whose
-    id lies outside 0..n-1 (-1 by custom) has no adapter.
+    id lies outside 0..n-1 (-1 by custom) has no adapter.  At least one row, as
+    gemm() takes.
 
     path as gemm()'s.  workspace: at least gemm_lora_workspace_size() bytes, for
     callers that manage their own; without one, each call takes a new block of
