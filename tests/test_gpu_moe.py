@@ -276,6 +276,29 @@ def test_experts_beyond_fp16_on_the_way(T, E, k, K, I, D, g, symmetric):
         assert not torch.isfinite(y[4]).any()
 
 
+@pytest.mark.parametrize("T", [1, 5, 90, 300])
+def test_experts_of_rows_that_are_not_finite(T):
+    """fp16: NaN and infinities in X, in routing weights and scales, without any
+    h that overflows: what the definition gives, NaN where it does."""
+    case = draw(T, 4, 2, 256, 136, 100, 128, "f16", False, seed=T)
+    X, ids, w, gu, dn = case
+    X[0, 3] = float("nan")
+    y = moe.experts(*on_gpu(case, 128)).cpu()
+    assert bool(y[0].isnan().all()) and bool(torch.isfinite(y[1:]).all())
+    X[0, 3] = 1.0
+    w[0, 0] = float("inf")
+    y = moe.experts(*on_gpu(case, 128)).cpu()
+    assert not torch.isfinite(y[0]).any() and bool(torch.isfinite(y[1:]).all())
+    w[0, 0] = 0.5
+    dn[1][:, 7] = float("inf")     # one column of every expert
+    y = moe.experts(*on_gpu(case, 128)).cpu()
+    assert not torch.isfinite(y[:, 7]).any()
+    rest = torch.cat([y[:, :7], y[:, 8:]], 1)
+    want, bound = ref.experts(X, ids, w, gu, (dn[0], torch.where(torch.isinf(dn[1]), 0.0, dn[1]).half(), dn[2]), 128)
+    want, bound = [torch.cat([t[:, :7], t[:, 8:]], 1) for t in (want, bound)]
+    assert bool(((rest.double() - want).abs() <= bound).all())
+
+
 def test_experts_is_repeatable_and_keeps_its_neighbours():
     """The same bits each time, into a caller's output and workspace, and
     nothing written before or behind them."""

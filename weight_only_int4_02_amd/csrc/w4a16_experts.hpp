@@ -191,6 +191,19 @@ __device__ __forceinline__ float wide_h(const ExpertsArgs &gu, int64_t t, int e,
     return silu(sum[0]) * sum[1];
 }
 
+// Whether a stored row of h holds an infinity (else what is not finite in its
+// results came from elsewhere, a NaN in X say, and they stand); the whole wave.
+__device__ __forceinline__ bool row_overflowed(const ExpertsArgs &dn, int64_t row, int lane) {
+    bool inf = false;
+    for (int i = 8 * lane; i < dn.K; i += 512) {
+        const h8_t h = *(const h8_t *)(dn.X + row * dn.K + i);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            inf = inf || __builtin_isinf((float)h[k]);
+    }
+    return __any(inf);
+}
+
 // Columns of h that a wave holds in LDS at once, in 32 bits.
 constexpr int kWideColumns = 1024;
 

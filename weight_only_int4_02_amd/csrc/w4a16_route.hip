@@ -475,8 +475,8 @@ __global__ __launch_bounds__(kPlanThreads) void expert_plan_kernel(
 // ---------------------------------------------------------------------------
 // Columns d .. d + C - 1 of row t once more, where an h beyond fp16 (or a routing
 // weight, X or W that is not finite) left one without a finite sum: the slots
-// whose results are not finite with h in 32 bits.  Stored where `in`; the whole
-// wave together.
+// whose h overflowed with it in 32 bits.  Stored where `in`; the whole wave
+// together.
 // The kernel's arguments are read again from their own memory, behind a pointer
 // that the compiler knows nothing about: in registers from the start they would
 // cost the kernel waves.
@@ -504,7 +504,7 @@ __device__ __forceinline__ void combine_wide(int64_t t, int64_t d, bool in) {
 #pragma unroll
         for (int c = 0; c < C; c++)
             whole = whole && __builtin_isfinite(p[c]);
-        if (__any(!whole))
+        if (__any(!whole) && row_overflowed(a.dn, row, lane))
             wide_dot<C>(a.gu, a.dn, t, row, id, weight, (int)d, lane, hs[threadIdx.x >> 6], sum);
         else
 #pragma unroll
