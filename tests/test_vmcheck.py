@@ -62,6 +62,33 @@ def test_scalar_wait_states_over_branches_and_other_writers():
 """) == []
 
 
+def test_a_matrix_instruction_right_after_its_operand_is_reported():
+    def mfma(body):
+        return vmcheck.check_asm_mfma("_Zkern:\n" + body.strip("\n") + "\n.Lfunc_end0:\n").get("_Zkern", [])
+
+    body = """
+    v_pk_mul_f16 v112, v122, v123
+    v_pk_mul_f16 v113, v4, v123
+    {}
+    ;;#ASMSTART
+    v_mfma_f32_16x16x32_f16 v[34:37], v[106:109], v[110:113], v[34:37]
+    v_mfma_f32_16x16x32_f16 v[30:33], v[102:105], v[110:113], v[30:33]
+    ;;#ASMEND
+    s_endpgm
+"""
+    f = mfma(body.format(""))
+    # v112 one wait state, v113 none for the first; for the second v113 one
+    assert [x[2] for x in f] == [[("v", 112), ("v", 113)], [("v", 113)]]
+    assert [x[2] for x in mfma(body.format("v_mul_u32_u24_e32 v3, 0x10001, v3"))] == [[("v", 113)]]
+    assert mfma(body.format("s_nop 1")) == [] and mfma(body.format("s_nop 4")) == []
+    # a matrix instruction's own result is not a vector write
+    assert mfma("""
+    v_mfma_f32_16x16x32_f16 v[34:37], v[106:109], v[110:113], v[34:37]
+    v_mfma_f32_16x16x32_f16 v[34:37], v[102:105], v[110:113], v[34:37]
+    s_endpgm
+""") == []
+
+
 def paths(body: str):
     asm = "_Zkern:\n" + body.strip("\n") + "\n.Lfunc_end0:\n"
     return vmcheck.check_asm_paths(asm).get("_Zkern", [])

@@ -84,8 +84,9 @@ def _check_inflight(src: str) -> None:
     same compile is checked against a model of the load counter
     (vmcheck.py), and any kernel that names such a register fails the build.
     So does one whose vector-memory instruction reads a scalar register sooner
-    than five wait states after a vector instruction wrote it: the compiler
-    does not keep that distance for inline assembly."""
+    than five wait states after a vector instruction wrote it, or whose matrix
+    instruction reads a vector register sooner than two: the compiler does not
+    keep those distances for inline assembly."""
     asm = os.path.join(BUILD_DIR, os.path.basename(src) + ".s")
     cmd = [HIPCC] + COMMON + ["-x", "hip", "--offload-device-only", "-S",
                               os.path.join(CSRC, src), "-o", asm]

@@ -103,12 +103,12 @@ __device__ __forceinline__ f4_t mfma16x16x32(h8_t a, h8_t b, f4_t c) {
 // lds_next + 4096 m).  FORM 1 (wait): a was filled by such a prefetch, so
 // MFMA m first waits until at most 7 - m LDS reads are outstanding (LDS
 // reads complete in order; the prefetch issued its eight in order m =
-// 0..7 and the caller issues no LDS read in between).
+// 0..7 and the caller issues no LDS read in between).  FORM 3: as 0, after
+// the wait states that a b written by compiled code needs.
 //
 // Hazards: no vector write lands in a register an MFMA of the block reads
 // (early clobbers); the returned operand's last write is two MFMAs before
-// the block ends (the next block's first MFMA reads it); the caller puts
-// wait states before a block whose b was written by compiled code.
+// the block ends (the next block's first MFMA reads it).
 // k: the masks 0x000F000F, 0x00F000F0 and 1/16 in both halves, in scalar
 // registers.
 struct UnpackConsts {
@@ -151,6 +151,8 @@ __device__ __forceinline__ h8_t mfma8_dequant(f4_t &c0, f4_t &c1, f4_t &c2, f4_t
     uint32_t bn0, bn1, bn2, bn3, t0, t1, t2, t3;
     if constexpr (FORM == 0)
         W4_DQ_BLOCK("", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
+    else if constexpr (FORM == 3)
+        W4_DQ_BLOCK("s_nop 1\n", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
     else if constexpr (FORM == 1)
         W4_DQ_BLOCK(W4_WT(7), "", W4_WT(6), "", W4_WT(5), "", W4_WT(4), "", W4_WT(3), "",
                     W4_WT(2), "", W4_WT(1), "", W4_WT(0), "");
@@ -232,7 +234,7 @@ __device__ __forceinline__ f4_t mfma16x16x32_bf16(bf8_t a, bf8_t b, f4_t c) {
 // the same instructions as dequant_word_bf16, in its element order -- spread
 // five or six after each of the first six MFMAs, and the same FORMs (0
 // plain, 1 wait for the prefetched fragments, 2 prefetch the next step's
-// fragments).  The last write of the returned operand is two MFMAs before
+// fragments, 3 plain after wait states).  The last write of the returned operand is two MFMAs before
 // the block ends; every temporary is an early clobber.  s and zf: the
 // tile's scale and zero in fp32; m: 0x0F0F0F0F in a scalar register.
 #define W4B_M(n) "v_mfma_f32_16x16x32_bf16 %[c" #n "], %[a" #n "], %[b], %[c" #n "]\n"
@@ -290,6 +292,8 @@ __device__ __forceinline__ h8_t mfma8_dequant_bf16(f4_t &c0, f4_t &c1, f4_t &c2,
     float f0, f1, f2, f3, f4, f5, f6, f7;
     if constexpr (FORM == 0)
         W4B_DQ_BLOCK("", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
+    else if constexpr (FORM == 3)
+        W4B_DQ_BLOCK("s_nop 1\n", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
     else if constexpr (FORM == 1)
         W4B_DQ_BLOCK(W4B_WT(7), "", W4B_WT(6), "", W4B_WT(5), "", W4B_WT(4), "", W4B_WT(3), "",
                      W4B_WT(2), "", W4B_WT(1), "", W4B_WT(0), "");

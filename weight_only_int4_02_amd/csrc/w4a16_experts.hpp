@@ -114,6 +114,8 @@ __device__ __forceinline__ h8_t mfma8_dequant_bf16_fma(f4_t &c0, f4_t &c1, f4_t 
     float f0, f1, f2, f3, f4, f5, f6, f7;
     if constexpr (FORM == 0)
         W4E_BLOCK("", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
+    else if constexpr (FORM == 3)
+        W4E_BLOCK("s_nop 1\n", "", "", "", "", "", "", "", "", "", "", "", "", "", "", "");
     else if constexpr (FORM == 1)
         W4E_BLOCK(W4E_WT(7), "", W4E_WT(6), "", W4E_WT(5), "", W4E_WT(4), "", W4E_WT(3), "",
                   W4E_WT(2), "", W4E_WT(1), "", W4E_WT(0), "");

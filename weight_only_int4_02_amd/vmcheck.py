@@ -29,7 +29,8 @@ instruction wrote that register.  The compiler keeps them for its own
 instructions and does not look into inline assembly, so a scalar register
 reloaded from a lane of a vector register (v_readlane_b32) right before an
 inline buffer load gives the load its old value: a wrong descriptor, and a
-memory fault.
+memory fault.  The same holds for an inline matrix instruction that reads a
+vector register: two wait states after the vector instruction that wrote it.
 """
 from __future__ import annotations
 
@@ -469,11 +470,30 @@ def _sgpr_step(state: Dict[int, int], ins: _Instr, report) -> Dict[int, int]:
     return state
 
 
-def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
-    """[(line, instruction, scalar registers it reads too early)], over every
-    path (the fewest wait states of the paths that merge)."""
+_MFMA_VGPR_WAIT_STATES = 2
+
+
+def _mfma_step(state: Dict[Reg, int], ins: _Instr, inline: FrozenSet[int], report) -> Dict[Reg, int]:
+    """state: vector register -> wait states since a vector instruction (no matrix
+    instruction) wrote it (below two).  Inline matrix instructions are reported."""
+    mfma = ins.op.startswith("v_mfma")
+    if state and mfma and ins.line in inline and report is not None:
+        early = sorted({r for ops in ins.ops[1:] for r in ops if r in state})
+        if early:
+            report(ins, early)
+    n = int(ins.text.split()[1], 0) + 1 if ins.op == "s_nop" else 1
+    state = {r: k + n for r, k in state.items() if k + n < _MFMA_VGPR_WAIT_STATES}
+    if ins.op.startswith("v_") and not mfma and ins.ops:
+        for r in ins.ops[0]:
+            state[r] = 0
+    return state
+
+
+def _check_wait_states(body: Sequence[Tuple[int, str]], step) -> List[Tuple[int, str, List[Reg]]]:
+    """What `step` reports, over every path (the fewest wait states of the paths
+    that merge)."""
     blocks, succs = _graph(body)
-    entry: List[Optional[Dict[int, int]]] = [None] * len(blocks)
+    entry: List[Optional[dict]] = [None] * len(blocks)
     if blocks:
         entry[0] = {}
     work = [0] if blocks else []
@@ -481,7 +501,7 @@ def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, 
         i = work.pop()
         q = dict(entry[i])
         for ins in blocks[i][1]:
-            q = _sgpr_step(q, ins, None)
+            q = step(q, ins, None)
         for j in succs[i]:
             old = entry[j]
             new = dict(q) if old is None else {r: min(q.get(r, 9), old.get(r, 9)) for r in q.keys() | old.keys()}
@@ -494,8 +514,19 @@ def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, 
         if q is None:
             continue
         for ins in blk[1]:
-            q = _sgpr_step(q, ins, lambda ins, regs: found.append((ins.line, ins.text, regs)))
+            q = step(q, ins, lambda ins, regs: found.append((ins.line, ins.text, regs)))
     return found
+
+
+def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
+    """[(line, vector-memory instruction, scalar registers it reads too early)]."""
+    return _check_wait_states(body, _sgpr_step)
+
+
+def check_kernel_mfma(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
+    """[(line, inline matrix instruction, vector registers it reads too early)]."""
+    inline = _inline_lines(body)
+    return _check_wait_states(body, lambda q, ins, report: _mfma_step(q, ins, inline, report))
 
 
 def kernels(asm: str) -> Dict[str, List[Tuple[int, str]]]:
@@ -527,6 +558,10 @@ def check_asm_sgprs(asm: str) -> Dict[str, List[Tuple[int, str, List[Reg]]]]:
     return {name: f for name, body in kernels(asm).items() for f in [check_kernel_sgprs(body)] if f}
 
 
+def check_asm_mfma(asm: str) -> Dict[str, List[Tuple[int, str, List[Reg]]]]:
+    return {name: f for name, body in kernels(asm).items() for f in [check_kernel_mfma(body)] if f}
+
+
 def demangle(name: str) -> str:
     try:
         return subprocess.run(["c++filt", name], capture_output=True, text=True).stdout.strip() or name
@@ -542,7 +577,8 @@ if __name__ == "__main__":
         text = open(path).read()
         for check, what in ((check_asm, "name registers of loads that may be in flight"),
                             (check_asm_paths, "name registers of loads before the first wait for them"),
-                            (check_asm_sgprs, "read scalar registers too soon after a vector write")):
+                            (check_asm_sgprs, "read scalar registers too soon after a vector write"),
+                            (check_asm_mfma, "are MFMAs that read registers too soon after a vector write")):
             for name, found in check(text).items():
                 bad += 1
                 print(f"{path}: {demangle(name)}: {len(found)} instructions {what}, "
