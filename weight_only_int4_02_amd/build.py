@@ -86,7 +86,7 @@ def _check_inflight(src: str) -> None:
     So does one whose vector-memory instruction reads a scalar register sooner
     than five wait states after a vector instruction wrote it, or whose matrix
     instruction reads a vector register sooner than two: the compiler does not
-    keep those distances for inline assembly."""
+    keep those distances where inline assembly is involved."""
     asm = os.path.join(BUILD_DIR, os.path.basename(src) + ".s")
     cmd = [HIPCC] + COMMON + ["-x", "hip", "--offload-device-only", "-S",
                               os.path.join(CSRC, src), "-o", asm]

@@ -176,6 +176,8 @@ __device__ __forceinline__ h8_t mfma8_dequant(f4_t &c0, f4_t &c1, f4_t &c2, f4_t
 // bit-exact, signed zeros and overflow included.  (fma(q, s, -z s) would
 // save an instruction but overflows in z s and loses the sign of zero.)
 typedef __bf16 bf8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 bf2_t __attribute__((ext_vector_type(2)));
+typedef float f2_t __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ float bf16_bits_to_float(uint32_t bits) {
     return __builtin_bit_cast(float, bits << 16);
@@ -191,14 +193,14 @@ __device__ __forceinline__ bf8_t dequant_word_bf16(uint32_t w, float s, float zf
                         (float)(hi & 0xFFu),         (float)((hi >> 16) & 0xFFu),
                         (float)((lo >> 8) & 0xFFu),  (float)(lo >> 24),
                         (float)((hi >> 8) & 0xFFu),  (float)(hi >> 24)};
-    // each pair rounded to bf16 by one v_cvt_pk_bf16_f32 (nearest-even),
-    // element 2p in the low half: written out so that the pairing never
-    // depends on how the compiler schedules the surrounding code
+    // each pair rounded to bf16 by one v_cvt_pk_bf16_f32 (nearest-even), element 2p
+    // in the low half.  Not inline: the compiler keeps the wait states that a
+    // matrix instruction needs after it.
     u4_t o;
 #pragma unroll
     for (int p = 0; p < 4; p++) {
         const float a = (q[2 * p] - zf) * s, b = (q[2 * p + 1] - zf) * s;
-        asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(o[p]) : "v"(a), "v"(b));
+        o[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, bf2_t));
     }
     return __builtin_bit_cast(bf8_t, o);
 }

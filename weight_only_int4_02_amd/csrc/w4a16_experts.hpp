@@ -46,7 +46,7 @@ __device__ __forceinline__ bf8_t dequant_word_bf16_fma(uint32_t w, Bf16Fma g) {
 #pragma unroll
     for (int p = 0; p < 4; p++) {
         const float a = __builtin_fmaf(q[2 * p], g.s, g.nzs), b = __builtin_fmaf(q[2 * p + 1], g.s, g.nzs);
-        asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(o[p]) : "v"(a), "v"(b));
+        o[p] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, bf2_t));
     }
     return __builtin_bit_cast(bf8_t, o);
 }

@@ -29,8 +29,9 @@ instruction wrote that register.  The compiler keeps them for its own
 instructions and does not look into inline assembly, so a scalar register
 reloaded from a lane of a vector register (v_readlane_b32) right before an
 inline buffer load gives the load its old value: a wrong descriptor, and a
-memory fault.  The same holds for an inline matrix instruction that reads a
-vector register: two wait states after the vector instruction that wrote it.
+memory fault.  The same holds for a matrix instruction that reads a vector
+register two wait states after the vector instruction that wrote it, where one
+of the two is inline.
 """
 from __future__ import annotations
 
@@ -473,11 +474,11 @@ def _sgpr_step(state: Dict[int, int], ins: _Instr, report) -> Dict[int, int]:
 _MFMA_VGPR_WAIT_STATES = 2
 
 
-def _mfma_step(state: Dict[Reg, int], ins: _Instr, inline: FrozenSet[int], report) -> Dict[Reg, int]:
+def _mfma_step(state: Dict[Reg, int], ins: _Instr, report) -> Dict[Reg, int]:
     """state: vector register -> wait states since a vector instruction (no matrix
-    instruction) wrote it (below two).  Inline matrix instructions are reported."""
+    instruction) wrote it (below two)."""
     mfma = ins.op.startswith("v_mfma")
-    if state and mfma and ins.line in inline and report is not None:
+    if state and mfma and report is not None:
         early = sorted({r for ops in ins.ops[1:] for r in ops if r in state})
         if early:
             report(ins, early)
@@ -524,9 +525,9 @@ def check_kernel_sgprs(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, 
 
 
 def check_kernel_mfma(body: Sequence[Tuple[int, str]]) -> List[Tuple[int, str, List[Reg]]]:
-    """[(line, inline matrix instruction, vector registers it reads too early)]."""
-    inline = _inline_lines(body)
-    return _check_wait_states(body, lambda q, ins, report: _mfma_step(q, ins, inline, report))
+    """[(line, matrix instruction, vector registers it reads too early)]: one of the
+    two instructions is inline, as the compiler keeps the distance of its own."""
+    return _check_wait_states(body, _mfma_step)
 
 
 def kernels(asm: str) -> Dict[str, List[Tuple[int, str]]]:
