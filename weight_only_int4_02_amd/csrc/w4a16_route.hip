@@ -30,7 +30,7 @@ namespace {
 // their logits at the end, one lane a slot, in 64 bits.
 //
 // The kernel is bound by its instructions and their latency, not its bytes
-// (8192 rows of 256 experts, 9 MB: 15.8 us, most of it the eight selections).  Few
+// (8192 rows of 256 experts, 9 MB: 15.9 us, most of it the eight selections).  Few
 // rows take a wave each, for the latency; many share waves, since the
 // reductions are the same work for all of a row's lanes.
 // ---------------------------------------------------------------------------
