@@ -276,6 +276,22 @@ def test_experts_beyond_fp16_on_the_way(T, E, k, K, I, D, g, symmetric):
         assert not torch.isfinite(y[4]).any()
 
 
+def test_experts_of_more_rows_than_one_grid_axis():
+    """The weighted sum's rows over two axes of its grid, one of the last rows
+    beyond fp16 on the way."""
+    T, E, k, K, I, D, g = 33000, 2, 2, 64, 64, 20, 32
+    X, ids, w, gu, dn = draw(T, E, k, K, I, D, g, "f16", False, seed=1, empty=0.1)
+    gu = (gu[0], (gu[1].double() * 100).half(), gu[2])
+    X = (X.double() / 40).half()
+    X[32900] = (X[32900].double() * 80).half()
+    ids[32900] = torch.tensor([1, 0])
+    case = X, ids, w, gu, (dn[0], (dn[1].double() / 64).half(), dn[2])
+    h = X[32900].double() @ ref.weight(*[t[1] for t in gu], g).T
+    assert (torch.nn.functional.silu(h[:I]) * h[I:]).abs().max() > 65504
+    y = check_experts(case, g)
+    assert torch.isfinite(y).all()
+
+
 @pytest.mark.parametrize("T", [1, 5, 90, 300])
 def test_experts_of_rows_that_are_not_finite(T):
     """fp16: NaN and infinities in X, in routing weights and scales, without any
