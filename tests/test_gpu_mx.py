@@ -1,0 +1,413 @@
+"""The microscaled 4-bit operators on the GPU against their definitions in 64
+bits (oracle/mx.py), whose bounds are derived there."""
+import pytest
+import torch
+
+from oracle import mx as ref
+from weight_only_int4_02_amd import moe, mx
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+INF, NAN = float("inf"), float("nan")
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def canonical(t):
+    """An MXTensor's element codes [.., K] and scale bytes [.., blocks], and that
+    its padding is zeros."""
+    codes, scales = t.codes.cpu(), t.scales.cpu()
+    code = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
+    blocks = -(-t.K // 32)
+    assert not bool(code[..., t.K:].any())
+    return code[..., :t.K], scales[..., :blocks]
+
+
+# ---- quantization -----------------------------------------------------------
+def check_quantize(x):
+    code, scale = canonical(mx.quantize(x.cuda()))
+    want_code, want_scale = ref.quantize(x)
+    assert torch.equal(scale, want_scale)
+    assert torch.equal(code, want_code)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("shape", [(1, 8), (1, 4096), (3, 24), (2, 40), (5, 136), (7, 1000), (257, 264),
+                                   (2, 3, 200), (33, 11008), (1025, 128)])
+def test_quantize(shape, dt):
+    x = torch.randn(shape, generator=gen(sum(shape)))
+    x = x * torch.exp2(torch.randint(-9, 9, shape[:-1] + (1,), generator=gen(1)).float())
+    check_quantize(x.to(DT[dt]))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_quantize_ties_and_borders(dt):
+    """Every multiple of 1/64 up to 8 (each border and tie among them), beside a
+    value that fixes the block's scale, at scales over the type's range."""
+    grid = torch.arange(-512, 513, dtype=torch.float64) / 64
+    grid = torch.nn.functional.pad(grid, (0, -len(grid) % 31)).reshape(-1, 31)
+    x = torch.cat([torch.full((len(grid), 1), 4.0, dtype=torch.float64), grid], 1)
+    for e in (-9, -2, 0, 3, 9) if dt == "f16" else (-110, -20, 0, 5, 119):
+        check_quantize((x * 2.0 ** e).to(DT[dt]))
+
+
+def test_quantize_over_the_whole_range_of_32_bits():
+    """Blocks of every exponent, subnormal ones among them: scales stop at 2^-127."""
+    e = torch.arange(-149, 128, dtype=torch.float64)[:, None]
+    x = torch.rand((len(e), 32), generator=gen(2), dtype=torch.float64) * 2 - 1
+    x[:, 5], x[:, 6], x[:, 7] = 1.0, -0.0, 0.0
+    check_quantize((x * 2.0 ** e).float())
+    top = torch.finfo(torch.float32).max
+    check_quantize(torch.tensor([[top, -top, top / 2, 1.0, 0.0, -0.0, 1e-30, -1e30]]))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_quantize_odd_values(dt):
+    x = torch.randn((8, 96), generator=gen(3))
+    x[0] = 0.0
+    x[1] = -0.0
+    x[2, 40] = INF                   # this block alone
+    x[3, 0] = NAN
+    x[4, 95] = -INF
+    x[5] = torch.finfo(DT[dt]).min
+    x[6] = torch.finfo(DT[dt]).tiny
+    x[7, 32:64] = 0.0
+    x = x.to(DT[dt])
+    check_quantize(x)
+    y = mx.dequantize(mx.quantize(x.cuda()), torch.float32).cpu()
+    assert bool(y[2, 32:64].isnan().all()) and not bool(y[2, :32].isnan().any())
+
+
+def test_quantize_no_rows():
+    t = mx.quantize(torch.empty((0, 64), device="cuda"))
+    assert t.codes.shape == (0, 64) and t.scales.shape == (0, 4)
+    assert mx.dequantize(t).shape == (0, 64)
+    assert mx.quantize(torch.empty((3, 0, 64), device="cuda", dtype=torch.float16)).shape == (3, 0, 64)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_dequantize_every_code_and_scale(dt):
+    code = torch.arange(16, dtype=torch.uint8).repeat(256, 3)[:, :40]
+    scale = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 2)
+    t = mx.tensor(ref.pack(code).cuda(), scale.cuda(), 40)
+    got = mx.dequantize(t, DT[dt]).cpu()
+    want = ref.values(code, scale).to(DT[dt])
+    assert torch.equal(got.isnan(), want.isnan())
+    assert torch.equal(got.nan_to_num(7.0), want.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
+def test_dequantized_values_quantize_to_themselves(dt):
+    x = torch.randn((9, 200), generator=gen(4)).to(DT[dt]).cuda()
+    t = mx.quantize(x)
+    u = mx.quantize(mx.dequantize(t, DT[dt]))
+    assert torch.equal(mx.dequantize(u, DT[dt]), mx.dequantize(t, DT[dt]))
+
+
+# ---- the weights' layout ------------------------------------------------------
+@pytest.mark.parametrize("E,N,K", [(1, 1, 8), (1, 33, 520), (3, 17, 136), (2, 16, 1024), (1, 100, 640)])
+def test_weight_layout(E, N, K):
+    code = torch.randint(0, 16, (E, N, K), generator=gen(N), dtype=torch.uint8)
+    scale = torch.randint(0, 256, (E, N, -(-K // 32)), generator=gen(K), dtype=torch.uint8)
+    t = mx.tensor(ref.pack(code).cuda(), scale.cuda(), K)
+    w = mx.weight(t)
+    NT, KT = -(-N // 16), -(-K // 128)
+    KG = -(-KT // 4)
+    q = torch.zeros((E, NT * 16, KT * 64), dtype=torch.uint8)
+    q[:, :N, :K // 2] = ref.pack(code)
+    q = q.reshape(E, NT, 16, KT, 4, 16).permute(0, 1, 3, 4, 2, 5).reshape(-1)
+    s = torch.full((E, NT * 16, KG * 16), 127, dtype=torch.uint8)
+    s[:, :N, :scale.shape[2]] = scale
+    s = s.reshape(E, NT, 16, KG, 16).permute(0, 1, 3, 2, 4).reshape(-1)
+    assert torch.equal(w.q.cpu(), q)
+    assert torch.equal(w.s.cpu(), s)
+
+
+# ---- products -----------------------------------------------------------------
+def random_weight(shape, seed, low=118, high=126):
+    code = torch.randint(0, 16, shape, generator=gen(seed), dtype=torch.uint8)
+    scale = torch.randint(low, high, (*shape[:-1], -(-shape[-1] // 32)), generator=gen(seed + 1), dtype=torch.uint8)
+    return code, scale
+
+
+def device_weight(code, scale):
+    return mx.weight(mx.tensor(ref.pack(code).cuda(), scale.cuda(), code.shape[-1]))
+
+
+def operands(x, code, scale, quantized):
+    """(what gemm is given for x, the values that x and W enter with)"""
+    W = ref.values(code, scale)
+    if quantized:
+        return mx.quantize(x.cuda()), ref.values(*ref.quantize(x)), W
+    return x.cuda(), x.double(), W.to(x.dtype).double()
+
+
+def compare(y, want, bound):
+    y = y.cpu().double()
+    assert torch.equal(y.isnan(), want.isnan())
+    fine = want.isfinite()
+    off = (y - want).abs()[fine]
+    assert bool((off <= bound[fine]).all()), float((off / bound[fine]).max())
+    rest = ~fine & ~want.isnan()
+    assert torch.equal(y[rest], want[rest])
+
+
+def check_gemm(M, N, K, dt, quantized, seed=0):
+    x = torch.randn((M, K), generator=gen(seed)).to(DT[dt])
+    code, scale = random_weight((N, K), seed + 1)
+    X, xv, wv = operands(x, code, scale, quantized)
+    y = mx.gemm(X, device_weight(code, scale))
+    assert y.dtype == DT[dt]
+    compare(y, *ref.product(xv, wv, DT[dt]))
+
+
+SHAPES = [(1, 1, 8), (1, 16, 128), (1, 64, 4096), (2, 33, 520), (5, 100, 136), (16, 48, 1024), (17, 70, 264),
+          (33, 257, 640), (61, 130, 1000), (64, 256, 2048), (65, 300, 1032), (128, 256, 512), (129, 259, 384),
+          (200, 515, 200), (300, 64, 72), (513, 100, 1160), (1, 4100, 11008), (40, 40, 11008)]
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_gemm(M, N, K, dt, quantized):
+    check_gemm(M, N, K, dt, quantized, seed=M + N)
+
+
+def test_gemm_types():
+    """fp32 rows quantize to bf16 results, and dtype names others."""
+    x = torch.randn((9, 160), generator=gen(5))
+    code, scale = random_weight((20, 160), 6)
+    w, t = device_weight(code, scale), mx.quantize(x.cuda())
+    xv, wv = ref.values(*ref.quantize(x)), ref.values(code, scale)
+    assert mx.gemm(t, w).dtype == torch.bfloat16
+    for dtype in (torch.float16, torch.bfloat16):
+        compare(mx.gemm(t, w, dtype=dtype), *ref.product(xv, wv, dtype))
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("M", [3, 40, 150])
+def test_gemm_odd_values(M, quantized):
+    """Infinities and NaN stay in the rows and columns that hold them, also in the
+    last columns of a K that ends inside a tile."""
+    N, K = 70, 328
+    x = torch.randn((M, K), generator=gen(7)).to(torch.bfloat16)
+    code, scale = random_weight((N, K), 8)
+    x[1, K - 1] = NAN
+    scale[5, -1] = 255
+    scale[69, 0] = 255
+    if not quantized:
+        x[2, 3] = INF
+        code[:, 3] = 2              # (no zero meets it)
+    X, xv, wv = operands(x, code, scale, quantized)
+    y = mx.gemm(X, device_weight(code, scale))
+    want, bound = ref.product(xv, wv, torch.bfloat16)
+    compare(y, want, bound)
+    assert bool(y[0, 0].isfinite()) and bool(y[1].isnan().all())
+
+
+@pytest.mark.parametrize("M", [4, 100])
+def test_gemm_scales_over_the_range(M):
+    """fp16: weights round to the type, subnormal and infinite ones too; MXFP4:
+    the extremes of the scales cancel; bf16: results past the type's range."""
+    N, K = 24, 96
+    code, scale = random_weight((N, K), 9, 95, 112)
+    x = torch.randn((M, K), generator=gen(10)).to(torch.float16)
+    X, xv, wv = operands(x, code, scale, False)
+    compare(mx.gemm(X, device_weight(code, scale)), *ref.product(xv, wv, torch.float16))
+    code, scale = random_weight((N, K), 11, 236, 244)
+    big = (torch.randn((M, K), generator=gen(12)).double() * 2.0 ** -110).to(torch.bfloat16)
+    for quantized in (False, True):
+        X, xv, wv = operands(big, code, scale, quantized)
+        compare(mx.gemm(X, device_weight(code, scale)), *ref.product(xv, wv, torch.bfloat16))
+
+
+def test_gemm_out_and_no_rows():
+    code, scale = random_weight((40, 64), 13)
+    w = device_weight(code, scale)
+    x = torch.randn((6, 64), generator=gen(14)).half().cuda()
+    out = torch.full((6, 40), 9.0, dtype=torch.float16, device="cuda")
+    assert mx.gemm(x, w, out=out) is out
+    assert torch.equal(out, mx.gemm(x, w))
+    assert mx.gemm(x[:0], w).shape == (0, 40)
+    assert mx.gemm(mx.quantize(x[:0]), w).shape == (0, 40)
+
+
+# ---- products grouped by expert -----------------------------------------------
+def check_grouped(T, counts, N, K, dt, quantized, gather, first=0, behind=0, seed=0, bad_rows=False):
+    E, R = len(counts), first + sum(counts) + behind
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32) + first
+    x = torch.randn((T if gather else R, K), generator=gen(seed)).to(DT[dt])
+    rows = None
+    if gather:
+        rows = torch.randint(0, T, (R,), generator=gen(seed + 1), dtype=torch.int32)
+        if bad_rows:
+            rows[::5], rows[1::7] = -1, T
+            rows[2::11] = -2 ** 31
+            rows[3::13] = 2 ** 31 - 1
+    code, scale = random_weight((E, N, K), seed + 2)
+    X, xv, wv = operands(x, code, scale, quantized)
+    out = torch.full((R, N), 77.0, dtype=DT[dt], device="cuda")
+    got = mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(),
+                          rows=None if rows is None else rows.cuda(), out=out)
+    assert got is out
+    want, bound, written = ref.grouped(xv, wv, offsets, rows, DT[dt])
+    compare(out[written.cuda()], want[written], bound[written])
+    assert bool((out.cpu()[~written] == 77.0).all())
+
+
+COUNTS = [[1], [0, 2], [3, 0, 0, 1], [1, 16, 17, 0, 5], [0, 0, 40, 0], [33, 1, 130, 0, 7], [129, 300, 0, 128],
+          [2] * 70, [0] * 200 + [5] + [0] * 100]
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"E{len(c)}R{sum(c)}")
+def test_grouped(counts, gather, quantized):
+    dt = "f16" if len(counts) % 2 else "bf16"
+    check_grouped(13, counts, 45, 264, dt, quantized, gather, seed=len(counts))
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("counts", [[4, 0, 9], [70, 90, 10]])
+def test_grouped_rows_of_no_expert_stay(counts, quantized):
+    for gather in (False, True):
+        check_grouped(21, counts, 34, 136, "bf16", quantized, gather, first=3, behind=20, seed=5)
+    check_grouped(21, [0, 0, 0], 34, 136, "f16", quantized, True, first=0, behind=9, seed=6)
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("counts", [[11, 30], [200, 150]])
+def test_grouped_indices_outside(counts, quantized):
+    check_grouped(17, counts, 40, 160, "f16", quantized, True, seed=7, bad_rows=True)
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_grouped_offsets_outside_stay_in_bounds(quantized):
+    """Offsets below 0 or past R count as the ends; falling ones leave an expert
+    without rows."""
+    N, K, R = 40, 72, 30
+    x = torch.randn((R, K), generator=gen(20)).half()
+    code, scale = random_weight((4, N, K), 21)
+    X, xv, wv = operands(x, code, scale, quantized)
+    guard = torch.full((R + 64, N), 77.0, dtype=torch.float16, device="cuda")
+    offsets = torch.tensor([-2 ** 31, 10, 10, 5, 2 ** 31 - 1], dtype=torch.int32)
+    mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(), out=guard[:R])
+    assert bool((guard[R:] == 77.0).all())
+    want, bound = ref.product(xv[:5], wv[0], torch.float16)    # (rows that one expert has)
+    compare(guard[:5], want, bound)
+    want, bound = ref.product(xv[10:], wv[3], torch.float16)
+    compare(guard[10:R], want, bound)
+
+
+def test_grouped_many_experts():
+    counts = torch.zeros(1024, dtype=torch.int64)
+    counts[torch.randint(0, 1024, (90,), generator=gen(22))] += 1
+    counts[1023], counts[0] = 40, 3
+    check_grouped(50, counts.tolist(), 20, 40, "bf16", True, True, seed=23)
+
+
+def test_grouped_no_rows():
+    w = device_weight(*random_weight((3, 24, 64), 24))
+    offsets = torch.zeros(4, dtype=torch.int32, device="cuda")
+    x = torch.randn((5, 64), device="cuda").half()
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    assert mx.grouped_gemm(x, w, offsets, rows=none).shape == (0, 24)
+    assert mx.grouped_gemm(x[:0], w, offsets).shape == (0, 24)
+
+
+# ---- together -------------------------------------------------------------------
+def expert_layer(x, logits, k, gate_up, down, quantized):
+    """A layer of gated experts from the operators, as a serving program has it;
+    what its steps were given and gave."""
+    E, T = gate_up.E, x.shape[0]
+    ids, weights = moe.route(logits, k)
+    flat = ids.reshape(-1)
+    order = flat.sort(stable=True).indices
+    offsets = torch.searchsorted(flat[order], torch.arange(E + 1, dtype=torch.int32, device=x.device)).to(torch.int32)
+    rows = (order // k).to(torch.int32)
+    gu = mx.grouped_gemm(mx.quantize(x) if quantized else x, gate_up, offsets, rows=rows)
+    gate, up = gu.float().chunk(2, dim=1)
+    h = (torch.nn.functional.silu(gate) * up).to(x.dtype)
+    d = mx.grouped_gemm(mx.quantize(h) if quantized else h, down, offsets)
+    share = weights.reshape(-1)[order]
+    y = torch.zeros((T, down.N), device=x.device).index_add_(0, rows, d.float() * share[:, None]).to(x.dtype)
+    return ids, offsets, rows, gu, h, d, share, y
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("T", [1, 50, 700])
+def test_expert_layer(T, quantized):
+    E, k, K, I = 6, 2, 160, 96
+    x = torch.randn((T, K), generator=gen(30)).to(torch.bfloat16)
+    logits = torch.randn((T, E), generator=gen(31))
+    gu_w, dn_w = random_weight((E, 2 * I, K), 32), random_weight((E, K, I), 33)
+    out = expert_layer(x.cuda(), logits.cuda(), k, device_weight(*gu_w), device_weight(*dn_w), quantized)
+    ids, offsets, rows, gu, h, d, share, y = (t.cpu() for t in out)
+    assert int(offsets[-1]) == T * k
+    for e in range(E):
+        mine = rows[offsets[e]:offsets[e + 1]].long()
+        assert bool((ids[mine] == e).any(1).all())
+    fake = (lambda v: ref.values(*ref.quantize(v))) if quantized else (lambda v: v.double())
+    want, bound, _ = ref.grouped(fake(x), ref.values(*gu_w), offsets, rows, torch.bfloat16)
+    compare(gu, want, bound)
+    want, bound, _ = ref.grouped(fake(h), ref.values(*dn_w), offsets, None, torch.bfloat16)
+    compare(d, want, bound)
+    terms = d.double() * share.double()[:, None]
+    want = torch.zeros((T, K), dtype=torch.float64).index_add_(0, rows.long(), terms)
+    size = torch.zeros((T, K), dtype=torch.float64).index_add_(0, rows.long(), terms.abs())
+    # k products and k sums in 32 bits, one rounding to bf16
+    compare(y, want, 2 * k * ref.U32 * size * 2 + 2.0 ** -8 * want.abs())
+
+
+def test_two_streams_at_once():
+    code, scale = random_weight((300, 520), 40)
+    w = device_weight(code, scale)
+    xs = [torch.randn((M, 520), generator=gen(M)).half().cuda() for M in (3, 90, 200)]
+    want = [mx.gemm(mx.quantize(x), w) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [None] * len(xs)
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i] = mx.gemm(mx.quantize(xs[i]), w)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [4, 150])
+def test_captured_and_replayed(T):
+    E, k, K, N = 5, 2, 264, 96
+    code, scale = random_weight((E, N, K), 50)
+    w = device_weight(code, scale)
+    x = torch.randn((T, K), generator=gen(51)).to(torch.bfloat16).cuda()
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    rows = torch.zeros(T * k, dtype=torch.int32, device="cuda")
+
+    def fill(seed):
+        ids = torch.randint(0, E, (T * k,), generator=gen(seed))
+        order = ids.sort(stable=True).indices
+        offsets.copy_(torch.tensor([0] + torch.bincount(ids, minlength=E).tolist()).cumsum(0).to(torch.int32))
+        rows.copy_((order // k).to(torch.int32))
+        x.copy_(torch.randn((T, K), generator=gen(seed + 1)).to(torch.bfloat16))
+
+    def step():
+        t = mx.quantize(x)
+        return mx.grouped_gemm(x, w, offsets, rows=rows), mx.grouped_gemm(t, w, offsets, rows=rows), mx.dequantize(t)
+
+    fill(52)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (53, 60, 70):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [o.clone() for o in out]
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))

@@ -28,7 +28,9 @@ SOURCES = ["w4a16_host.cpp", "w4a16_api.hip", "w4a16_kernels.hip", "w4a16_gemm.h
            "w4a16_lora.hip",
            "w4a16_small_jpg1_lora.hip", "w4a16_small_jpg2_lora.hip", "w4a16_small_jpg4_lora.hip",
            "w4a16_small_jpg1_bf16_lora.hip", "w4a16_small_jpg2_bf16_lora.hip",
-           "w4a16_small_jpg4_bf16_lora.hip", "w4a16_large_lora.hip", "w4a16_large_bf16_lora.hip"]
+           "w4a16_small_jpg4_bf16_lora.hip", "w4a16_large_lora.hip", "w4a16_large_bf16_lora.hip",
+           "w4a16_mx_host.cpp", "w4a16_mx_api.hip", "w4a16_mx_quantize.hip", "w4a16_mx_small.hip",
+           "w4a16_mx_large.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 # One target only.  Packed fp32 instructions are switched off for the device

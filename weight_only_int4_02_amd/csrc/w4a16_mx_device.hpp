@@ -1,0 +1,162 @@
+// Device helpers shared by the microscaled 4-bit kernels.
+//
+// gfx950 converts between E2M1 and wider types in one instruction per pair of
+// values, with the scale applied: v_cvt_scalef32_* take the scale's power of two
+// from the exponent field of an fp32 register (0 there means 2^-127, 255 NaN), so
+// an E8M0 byte moved to bits 23..30 is that register.  They round to nearest
+// even and saturate where E2M1 is the result.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "w4a16_gemm_kernels.hpp"
+#include "w4a16_mx.hpp"
+
+namespace w4a16 {
+
+typedef int32_t i8_t __attribute__((ext_vector_type(8)));
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
+
+// Byte `b` of a register of four scales as the scale operand of a conversion.
+__device__ __forceinline__ float mx_scale(uint32_t scales, uint32_t b) {
+    return __builtin_bit_cast(float, ((scales >> (8 * b)) & 0xFFu) << 23);
+}
+
+// The eight values of a code word times the scale, in the 16-bit type.
+template <bool BF>
+__device__ __forceinline__ u4_t mx_decode(uint32_t w, float s) {
+    u4_t o;
+    if constexpr (BF) {
+        o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+        o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+        o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+        o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+    } else {
+        o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0));
+        o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1));
+        o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2));
+        o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3));
+    }
+    return o;
+}
+
+// 16 x 16 results of 128 columns of two MXFP4 operands; byte 0 of sa and sb is
+// the scale of the lane's block.
+__device__ __forceinline__ f4_t mx_mfma16(u4_t a, u4_t b, f4_t c, uint32_t sa, uint32_t sb) {
+    const i8_t A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w}, B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
+}
+
+// 32 x 32 results of 64 columns; byte SEL of sa and sb.
+template <int SEL>
+__device__ __forceinline__ f16_t mx_mfma32(u4_t a, u4_t b, f16_t c, uint32_t sa, uint32_t sb) {
+    const i8_t A = {(int)a.x, (int)a.y, (int)a.z, (int)a.w}, B = {(int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(A, B, c, 4, 4, SEL, (int)sa, SEL, (int)sb);
+}
+
+template <bool BF>
+__device__ __forceinline__ uint32_t mx_pack2(float a, float b) {
+    if constexpr (BF)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, bf2_t));
+    else
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, h2_t));
+}
+
+// Four neighbouring results of one row, rounded and stored: columns n .. n + 3
+// of the row at y (of N columns); n is a multiple of 4.
+template <bool BF>
+__device__ __forceinline__ void mx_store4(uint16_t *y, int n, int N, float v0, float v1, float v2,
+                                          float v3) {
+    const u2_t v = {mx_pack2<BF>(v0, v1), mx_pack2<BF>(v2, v3)};
+    if ((N & 3) == 0) {     // (rows are aligned to 8 bytes)
+        if (n < N)
+            *(u2_t *)(y + n) = v;
+    } else {
+        if (n < N)
+            y[n] = (uint16_t)v.x;
+        if (n + 1 < N)
+            y[n + 1] = (uint16_t)(v.x >> 16);
+        if (n + 2 < N)
+            y[n + 2] = (uint16_t)v.y;
+        if (n + 3 < N)
+            y[n + 3] = (uint16_t)(v.y >> 16);
+    }
+}
+
+// A row tile of a product: matrix e has the rows from `start` on, `total` of
+// them, in `count` tiles of BM; the tile is the mt-th, rows row0 .. row0 + rows - 1.
+// All are held within 0 .. R.
+struct MxTile {
+    int e, start, total, count;
+    int mt, row0, rows;
+    __device__ __forceinline__ void take(int tile, int bm) {
+        mt = tile;
+        row0 = start + tile * bm;
+        rows = total - tile * bm < bm ? total - tile * bm : bm;
+    }
+};
+
+// Rows of matrix e: offsets outside 0 .. R are taken as the ends.
+__device__ __forceinline__ int mx_offset(const MxArgs &a, int e) {
+    const int o = a.offsets[e];
+    return o < 0 ? 0 : o > (int)a.R ? (int)a.R : o;
+}
+
+// Sum over the wave's lanes up to the own one.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int o = __shfl_up(v, d);
+        v += lane >= d ? o : 0;
+    }
+    return v;
+}
+
+// How many tiles of BM rows all matrices have together (by one wave).
+template <int BM>
+__device__ __forceinline__ int mx_count_tiles(const MxArgs &a, int lane) {
+    int total = 0;
+    for (int base = 0; base < a.E; base += 64) {
+        const int e = base + lane;
+        int n = 0;
+        if (e < a.E) {
+            const int r = mx_offset(a, e + 1) - mx_offset(a, e);
+            n = r > 0 ? (r + BM - 1) / BM : 0;
+        }
+        total += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
+    }
+    return total;
+}
+
+// Tile `t` of all matrices' (by one wave; t is the same in all lanes); count 0
+// where there are not so many.
+template <int BM>
+__device__ __forceinline__ MxTile mx_find_tile(const MxArgs &a, int t, int lane) {
+    MxTile out = {};
+    int before = 0;
+    for (int base = 0; base < a.E; base += 64) {
+        const int e = base + lane;
+        int n = 0, o = 0, r = 0;
+        if (e < a.E) {
+            o = mx_offset(a, e);
+            r = mx_offset(a, e + 1) - o;
+            n = r > 0 ? (r + BM - 1) / BM : 0;
+        }
+        const int incl = before + wave_scan(n, lane);
+        const uint64_t past = __ballot(incl > t);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            out.e = base + l;
+            out.start = __builtin_amdgcn_readlane(o, l);
+            out.total = __builtin_amdgcn_readlane(r, l);
+            out.count = __builtin_amdgcn_readlane(n, l);
+            out.take(t - (__builtin_amdgcn_readlane(incl, l) - out.count), BM);
+            return out;
+        }
+        before = __builtin_amdgcn_readlane(incl, 63);
+    }
+    return out;
+}
+
+}  // namespace w4a16

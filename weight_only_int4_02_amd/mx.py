@@ -1,0 +1,303 @@
+"""Microscaled 4-bit floating point (MXFP4): quantization, products, products
+grouped by expert.
+
+    X [.., K] fp16, bf16 or fp32       -> quantize()     -> MXTensor
+    codes, scales of a checkpoint      -> tensor()       -> MXTensor
+    MXTensor                           -> dequantize()   -> X [.., K]
+    MXTensor [N, K] or [E, N, K]       -> weight()       -> MXWeight (device layout)
+    X [M, K] or MXTensor, MXWeight     -> gemm()         -> Y [M, N]
+    X, MXWeight of E, offsets          -> grouped_gemm() -> Y [R, N]
+
+The format is that of the Open Compute Project's microscaling specification:
+blocks of 32 columns, 4-bit elements (sign; 0, 0.5, 1, 1.5, 2, 3, 4 or 6), a
+power of two a block.  A thin binding over libw4a16.so (C ABI in
+include/w4a16_mx.h): arguments are checked and marshalled here, every step runs
+in the library's HIP kernels on the current stream.  Serving only: no
+gradients are formed.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _raise, lib
+from .moe import check, stream_of
+
+BLOCK = 32
+MAX_EXPERTS = 1024
+
+# Symbols of include/w4a16_mx.h.
+EXPORTS = ("w4a16_mx_quantize", "w4a16_mx_check_quantize_args", "w4a16_mx_dequantize",
+           "w4a16_mx_check_dequantize_args", "w4a16_mx_weight_size", "w4a16_mx_weight",
+           "w4a16_mx_check_weight_args", "w4a16_mx_gemm", "w4a16_mx_check_gemm_args",
+           "w4a16_mx_grouped_gemm", "w4a16_mx_check_grouped_gemm_args")
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+
+_bound = None
+
+
+def _mx():
+    """libw4a16.so with this module's argument types set."""
+    global _bound
+    if _bound is None:
+        L = lib()
+        P, I64, I32, PSZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)
+        args = {"quantize": [P, I32, I64, I64, P, P], "dequantize": [P, P, I64, I64, I32, P],
+                "weight": [P, P, I64, I64, I64, P, P],
+                "gemm": [P, P, I32, I64, I64, P, P, I64, I32, P],
+                "grouped_gemm": [P, P, I32, I64, I64, P, I64, P, I64, P, P, I64, I32, P]}
+        for name, types in args.items():
+            getattr(L, f"w4a16_mx_{name}").argtypes = types + [P]
+            getattr(L, f"w4a16_mx_check_{name}_args").argtypes = types
+        L.w4a16_mx_weight_size.argtypes = [I64, I64, I64, PSZ, PSZ]
+        for name in EXPORTS:
+            getattr(L, name).restype = I32
+        _bound = L
+    return _bound
+
+
+@dataclass
+class MXTensor:
+    """MXFP4 rows, owned by torch tensors: codes uint8 [.., 64 KT] (two columns a
+    byte, the first in the low half) and scales uint8 [.., 4 KT] (2^(b - 127), 255
+    for NaN), KT = ceil(K / 128); columns from K on hold zeros.  dtype: the type
+    dequantize() and products give where none is named."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    K: int
+    dtype: torch.dtype = torch.bfloat16
+
+    @property
+    def shape(self):
+        return (*self.codes.shape[:-1], self.K)
+
+
+@dataclass
+class MXWeight:
+    """E matrices [N, K] in the device layout, owned by torch tensors."""
+    q: torch.Tensor
+    s: torch.Tensor
+    E: int
+    N: int
+    K: int
+
+
+def _tiles(K: int) -> int:
+    return -(-K // 128)
+
+
+def _float_type(dtype, types, name: str) -> int:
+    if dtype not in _DTYPES or dtype not in types:
+        raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}, got {dtype}")
+    return _DTYPES[dtype]
+
+
+def _check_tensor(t, name: str, device: int, ndim: Optional[int] = None) -> None:
+    """The tensors of an MXTensor hold what its shape needs (the kernels read
+    them through bare pointers)."""
+    if not isinstance(t, MXTensor):
+        raise TypeError(f"{name} must be an MXTensor")
+    ndim = t.codes.dim() if ndim is None else ndim
+    check(t.codes, f"{name}.codes", torch.uint8, ndim, device)
+    check(t.scales, f"{name}.scales", torch.uint8, ndim, device)
+    KT = _tiles(t.K)
+    if (t.codes.shape[:-1] != t.scales.shape[:-1] or t.codes.shape[-1] != 64 * KT
+            or t.scales.shape[-1] != 4 * KT):
+        raise ValueError(f"{name}: codes must be [.., {64 * KT}] and scales [.., {4 * KT}] for K = {t.K}, "
+                         f"got {tuple(t.codes.shape)} and {tuple(t.scales.shape)}")
+
+
+def quantize(x: torch.Tensor) -> MXTensor:
+    """x [.., K] (fp16, bf16 or fp32, contiguous, K a multiple of 8) -> MXTensor.
+
+    A block's scale is 2^(floor(log2 a) - 2) for its largest magnitude a; its
+    elements are rounded to nearest, ties to even, beyond 6 scales to 6.  A block
+    that holds an infinity or a NaN becomes NaN throughout.  There may be no
+    rows; the last block of a row may be partial."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dt = _float_type(x.dtype, tuple(_DTYPES), "x")
+    if x.dim() < 1 or not x.is_cuda:
+        raise ValueError("x must be a device tensor of at least one dimension")
+    device = x.get_device()
+    check(x, "x", x.dtype, x.dim(), device)
+    stream = stream_of(device)
+    K = x.shape[-1]
+    if K < 1 or K % 8:
+        raise ValueError("K must be a positive multiple of 8")
+    M, KT = x.numel() // K, _tiles(K)
+    codes = torch.empty((*x.shape[:-1], 64 * KT), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], 4 * KT), dtype=torch.uint8, device=x.device)
+    if M:
+        _raise(_mx().w4a16_mx_quantize(x.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr(), stream),
+               "w4a16_mx_quantize")
+    return MXTensor(codes, scales, K, torch.bfloat16 if x.dtype == torch.float32 else x.dtype)
+
+
+def dequantize(t: MXTensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """The values of t [.., K], in dtype (t.dtype if None), each rounded once:
+    exact in bf16 and fp32, but for magnitudes past the type's largest."""
+    if not isinstance(t, MXTensor):
+        raise TypeError("t must be an MXTensor")
+    if not t.codes.is_cuda:
+        raise ValueError("t must be on a device")
+    dtype = t.dtype if dtype is None else dtype
+    dt = _float_type(dtype, tuple(_DTYPES), "dtype")
+    device = t.codes.get_device()
+    _check_tensor(t, "t", device)
+    stream = stream_of(device)
+    out = torch.empty(t.shape, dtype=dtype, device=t.codes.device)
+    M = out.numel() // t.K
+    if M:
+        _raise(_mx().w4a16_mx_dequantize(t.codes.data_ptr(), t.scales.data_ptr(), M, t.K, dt, out.data_ptr(),
+                                         stream), "w4a16_mx_dequantize")
+    return out
+
+
+def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
+           dtype: torch.dtype = torch.bfloat16) -> MXTensor:
+    """codes uint8 [.., K/2] and scales uint8 [.., ceil(K/32)], as checkpoints hold
+    them, on the device -> MXTensor (padded to whole tiles of 128 columns).  K:
+    twice the codes' last dimension if None."""
+    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() < 1:
+        raise ValueError("codes must be a device tensor of at least one dimension")
+    device = codes.get_device()
+    check(codes, "codes", torch.uint8, codes.dim(), device)
+    check(scales, "scales", torch.uint8, codes.dim(), device)
+    _float_type(dtype, (torch.float16, torch.bfloat16), "dtype")
+    K = 2 * codes.shape[-1] if K is None else K
+    if K < 1 or K % 8:
+        raise ValueError("K must be a positive multiple of 8")
+    if (codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != K // 2
+            or scales.shape[-1] != -(-K // BLOCK)):
+        raise ValueError("codes must be [.., K/2] and scales [.., ceil(K/32)]")
+    KT = _tiles(K)
+    if codes.shape[-1] != 64 * KT:
+        codes = torch.nn.functional.pad(codes, (0, 64 * KT - codes.shape[-1]))
+    if scales.shape[-1] != 4 * KT:
+        scales = torch.nn.functional.pad(scales, (0, 4 * KT - scales.shape[-1]), value=127)
+    return MXTensor(codes, scales, K, dtype)
+
+
+def weight_size(E: int, N: int, K: int):
+    q, s = ctypes.c_size_t(), ctypes.c_size_t()
+    _raise(_mx().w4a16_mx_weight_size(E, N, K, ctypes.byref(q), ctypes.byref(s)), "w4a16_mx_weight_size")
+    return q.value, s.value
+
+
+def weight(t: MXTensor) -> MXWeight:
+    """An MXTensor [N, K], or [E, N, K] for E experts, in the products' layout."""
+    if not isinstance(t, MXTensor):
+        raise TypeError("t must be an MXTensor")
+    if t.codes.dim() not in (2, 3):
+        raise ValueError("t must be [N, K] or [E, N, K]")
+    device = t.codes.get_device()
+    _check_tensor(t, "t", device)
+    stream = stream_of(device)
+    E, N = (1, *t.codes.shape[:-1]) if t.codes.dim() == 2 else t.codes.shape[:-1]
+    qb, sb = weight_size(E, N, t.K)
+    codes, scales = (x if x.data_ptr() % 16 == 0 else x.clone() for x in (t.codes, t.scales))
+    q = torch.empty(qb, dtype=torch.uint8, device=codes.device)
+    s = torch.empty(sb, dtype=torch.uint8, device=codes.device)
+    _raise(_mx().w4a16_mx_weight(codes.data_ptr(), scales.data_ptr(), E, N, t.K, q.data_ptr(), s.data_ptr(),
+                                 stream), "w4a16_mx_weight")
+    return MXWeight(q, s, E, N, t.K)
+
+
+def _check_weight(w: MXWeight, device: int) -> None:
+    if not isinstance(w, MXWeight):
+        raise TypeError("w must be an MXWeight")
+    check(w.q, "w.q", torch.uint8, 1, device)
+    check(w.s, "w.s", torch.uint8, 1, device)
+    nt, kt = -(-w.N // 16), _tiles(w.K)
+    if w.q.numel() < w.E * nt * kt * 1024 or w.s.numel() < w.E * nt * -(-kt // 4) * 256:
+        raise ValueError("MXWeight tensors are smaller than its shape needs")
+
+
+def _activations(x, K: int, dtype):
+    """(device, data, scales or None, x's dtype code, y's dtype code, y's dtype)"""
+    if isinstance(x, MXTensor):
+        device = x.codes.get_device()
+        _check_tensor(x, "x", device, 2)
+        dtype = x.dtype if dtype is None else dtype
+        data, scales, xt = x.codes, x.scales, 0
+    else:
+        if not isinstance(x, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor or an MXTensor")
+        xt = _float_type(x.dtype, (torch.float16, torch.bfloat16), "x")
+        device = x.get_device()
+        check(x, "x", x.dtype, 2, device)
+        if dtype not in (None, x.dtype):
+            raise TypeError("the results of 16-bit activations have their type")
+        dtype, data, scales = x.dtype, x, None
+    if device < 0:
+        raise ValueError("x must be on a device")
+    if x.shape[1] != K:
+        raise ValueError(f"x has K={x.shape[1]}, the weight K={K}")
+    return device, data, scales, xt, _float_type(dtype, (torch.float16, torch.bfloat16), "dtype"), dtype
+
+
+def gemm(x, w: MXWeight, out: Optional[torch.Tensor] = None,
+         dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Y [M, N] = x [M, K] . dequantize(w)^T, with fp32 sums.
+
+    x: fp16 or bf16, whose type Y has; the weights enter as their values in
+    that type (in fp16: subnormal below 2^-14, infinite from 65520 on).  Or an
+    MXTensor: both operands enter as they are, and Y has `dtype` (x.dtype if
+    None).  M may be 0."""
+    device, data, scales, xt, yt, dtype = _activations(x, w.K, dtype)
+    _check_weight(w, device)
+    if w.E != 1:
+        raise ValueError("a weight of several experts goes to grouped_gemm")
+    M = data.shape[0]
+    if out is None:
+        out = torch.empty((M, w.N), dtype=dtype, device=data.device)
+    else:
+        check(out, "out", dtype, 2, device)
+        if tuple(out.shape) != (M, w.N):
+            raise ValueError("out must be [M, N]")
+    stream = stream_of(device)
+    if M:
+        _raise(_mx().w4a16_mx_gemm(data.data_ptr(), None if scales is None else scales.data_ptr(), xt, M, w.K,
+                                   w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(), stream),
+               "w4a16_mx_gemm")
+    return out
+
+
+def grouped_gemm(x, w: MXWeight, offsets: torch.Tensor, rows: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """Y [R, N]: Y[i] = x[rows[i]] . dequantize(w_e)^T for offsets[e] <= i <
+    offsets[e + 1], the rows of expert e; without rows, Y[i] = x[i] . ...
+
+    x [T, K] as gemm()'s, offsets int32 [E + 1], rising from 0 or more to R or
+    less, rows int32 [R] (a row whose index lies outside 0..T-1 counts as
+    zeros).  An expert may have no rows.  Rows of Y that no expert has stay as they
+    are in `out`, and are undefined without one.  R may be 0."""
+    device, data, scales, xt, yt, dtype = _activations(x, w.K, dtype)
+    _check_weight(w, device)
+    check(offsets, "offsets", torch.int32, 1, device)
+    if offsets.shape[0] != w.E + 1:
+        raise ValueError("offsets must be [E + 1]")
+    T = R = data.shape[0]
+    if rows is not None:
+        check(rows, "rows", torch.int32, 1, device)
+        R = rows.shape[0]
+    if out is None:
+        out = torch.empty((R, w.N), dtype=dtype, device=data.device)
+    else:
+        check(out, "out", dtype, 2, device)
+        if tuple(out.shape) != (R, w.N):
+            raise ValueError("out must be [R, N]")
+    stream = stream_of(device)
+    if R and not T:
+        raise ValueError("x has no rows")
+    if R:
+        _raise(_mx().w4a16_mx_grouped_gemm(
+            data.data_ptr(), None if scales is None else scales.data_ptr(), xt, T, w.K,
+            None if rows is None else rows.data_ptr(), R, offsets.data_ptr(), w.E, w.q.data_ptr(),
+            w.s.data_ptr(), w.N, yt, out.data_ptr(), stream), "w4a16_mx_grouped_gemm")
+    return out
