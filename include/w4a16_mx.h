@@ -3,24 +3,27 @@
  * quantization to MXFP4, products of activations with MXFP4 weights, and
  * products grouped by expert.  Conventions and status codes are those of
  * w4a16.h (the caller owns every buffer, arguments are checked on the host
- * before any launch, work is enqueued on `stream`, nothing is allocated and no
- * workspace is needed).
+ * before any launch, work is enqueued on `stream`, nothing is allocated).
  *
  * MXFP4 (Open Compute Project, "Microscaling Formats", version 1.0): blocks of
  * 32 consecutive columns of a row.  An element is E2M1 (sign, and one of 0, 0.5,
  * 1, 1.5, 2, 3, 4, 6 by its number 0..7), a block's scale E8M0: byte b stands
  * for 2^(b - 127), 255 for NaN.  A value is element times scale.
  *
- * Rows are held in whole 128-column tiles, KT = ceil(K / 128):
- *   codes   uint8 [rows][64 KT], two columns a byte, the first in the low half;
- *   scales  uint8 [rows][4 KT], a byte a block.
- * Columns from K on hold zeros.  K is a multiple of 8 (the last block may be
- * partial).
+ * Rows are held in whole slabs of 512 columns, KG = ceil(K / 512):
+ *   codes   uint8 [2 KG][rows][128], of 256 columns the 128 bytes of a row, two
+ *           columns a byte, the first in the low half;
+ *   scales  uint8 [KG][rows][16], the slab's 16 blocks of a row.
+ * Columns from K on hold zeros (their scales: any but 255).  K is a multiple of
+ * 8 (the last block may be partial).
  *
- * The device layout of a weight of N rows, NT = ceil(N / 16), KG = ceil(KT / 4):
- *   codes   [NT][KT][4][16][16]: of 16 rows by 128 columns, block b of row r is
- *           the 16 bytes at 16 (16 b + r);
- *   scales  [NT][KG][16][16]: of 16 rows by 512 columns, the 16 scales of a row.
+ * The device layout of a weight of N rows, NT = ceil(N / 16), KT = ceil(K / 128):
+ *   codes   [2 KT][NT][2][16][16]: of 64 columns and 16 rows, the 16 bytes of
+ *           each row's first block, then of its second;
+ *   scales  [KG][16 NT][16]: of 512 columns the 16 scales of each row.
+ * (What a tile of the products takes of 64 columns is one run of memory: with a
+ * row's columns together, the tiles of a column block lie a power of two apart
+ * for most K and share few of the L2's channels.)
  * Rows past N and columns past K hold zeros (scales: 127).
  */
 #ifndef W4A16_MX_H
@@ -43,9 +46,9 @@ extern "C" {
  * with the even number, a magnitude beyond 6 to 6.  The sign of a zero is
  * kept.  A block that holds an infinity or a NaN is NaN throughout: scale 255,
  * codes 0.
- * Limits: M < 2^31, K <= 2^24, M KT < 2^31.
- * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE, W4A16_ERR_ALIGN (X and codes 16
- * bytes, scales 4), W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * Limits: M < 2^31, K <= 2^24, 4 M KG < 2^31.
+ * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE, W4A16_ERR_ALIGN (16 bytes each),
+ * W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_mx_quantize(const void *X, int32_t dtype, int64_t M, int64_t K, uint8_t *codes,
                           uint8_t *scales, void *stream);
 int32_t w4a16_mx_check_quantize_args(const void *X, int32_t dtype, int64_t M, int64_t K,
@@ -59,8 +62,7 @@ int32_t w4a16_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t
 int32_t w4a16_mx_check_dequantize_args(const uint8_t *codes, const uint8_t *scales, int64_t M,
                                        int64_t K, int32_t dtype, const void *Y);
 
-/* E matrices [N][K] (codes and scales as above, one matrix after the other)
- * -> the device layout, one matrix after the other; w4a16_mx_weight_size has
+/* E matrices [N][K] (codes and scales as above, of E N rows) -> the device layout, one matrix after the other; w4a16_mx_weight_size has
  * the bytes of all E.
  * Limits: 1 <= E <= 1024, N < 2^22, K <= 2^20, one matrix's codes below 2 GiB. */
 int32_t w4a16_mx_weight_size(int64_t E, int64_t N, int64_t K, size_t *q_bytes, size_t *s_bytes);
@@ -75,16 +77,22 @@ int32_t w4a16_mx_check_weight_args(const uint8_t *codes, const uint8_t *scales, 
  *   else X and x_scales are MXFP4 rows, multiplied by the matrix cores' scaled
  *     instruction.
  * y_dtype: fp16 or bf16; of a 16-bit X, its own.
+ * workspace: w4a16_mx_gemm_workspace_size bytes (no fill needed, NULL where
+ * that is 0; quantized: x_scales given): fp32 sums of parts of K.  Calls that may
+ * run at the same time need separate ones.
  * Limits: those of w4a16_mx_weight, M < 2^31, X below 2 GiB.
  * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y overlaps X or its
- * scales), W4A16_ERR_ALIGN (X, q_dev, s_dev and Y 16 bytes, x_scales 4),
- * W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * scales), W4A16_ERR_ALIGN (16 bytes each), W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantized,
+                                     size_t *bytes);
 int32_t w4a16_mx_gemm(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t M,
                       int64_t K, const void *q_dev, const void *s_dev, int64_t N,
-                      int32_t y_dtype, void *Y, void *stream);
+                      int32_t y_dtype, void *Y, void *workspace, size_t workspace_bytes,
+                      void *stream);
 int32_t w4a16_mx_check_gemm_args(const void *X, const uint8_t *x_scales, int32_t x_dtype,
                                  int64_t M, int64_t K, const void *q_dev, const void *s_dev,
-                                 int64_t N, int32_t y_dtype, const void *Y);
+                                 int64_t N, int32_t y_dtype, const void *Y, const void *workspace,
+                                 size_t workspace_bytes);
 
 /* The products of E experts over rows that lie sorted by expert:
  *   Y[i] = X[rows[i]] . W_e^T   for offsets[e] <= i < offsets[e + 1]

@@ -20,7 +20,7 @@ def gen(seed):
 def canonical(t):
     """An MXTensor's element codes [.., K] and scale bytes [.., blocks], and that
     its padding is zeros."""
-    codes, scales = t.codes.cpu(), t.scales.cpu()
+    codes, scales = (p.cpu().movedim(0, -2).flatten(-2) for p in (t.codes, t.scales))
     code = torch.stack([codes & 15, codes >> 4], -1).flatten(-2)
     blocks = -(-t.K // 32)
     assert not bool(code[..., t.K:].any())
@@ -84,7 +84,7 @@ def test_quantize_odd_values(dt):
 
 def test_quantize_no_rows():
     t = mx.quantize(torch.empty((0, 64), device="cuda"))
-    assert t.codes.shape == (0, 64) and t.scales.shape == (0, 4)
+    assert t.codes.shape == (2, 0, 128) and t.scales.shape == (1, 0, 16)
     assert mx.dequantize(t).shape == (0, 64)
     assert mx.quantize(torch.empty((3, 0, 64), device="cuda", dtype=torch.float16)).shape == (3, 0, 64)
 
@@ -119,10 +119,10 @@ def test_weight_layout(E, N, K):
     KG = -(-KT // 4)
     q = torch.zeros((E, NT * 16, KT * 64), dtype=torch.uint8)
     q[:, :N, :K // 2] = ref.pack(code)
-    q = q.reshape(E, NT, 16, KT, 4, 16).permute(0, 1, 3, 4, 2, 5).reshape(-1)
+    q = q.reshape(E, NT, 16, 2 * KT, 2, 16).permute(0, 3, 1, 4, 2, 5).reshape(-1)
     s = torch.full((E, NT * 16, KG * 16), 127, dtype=torch.uint8)
     s[:, :N, :scale.shape[2]] = scale
-    s = s.reshape(E, NT, 16, KG, 16).permute(0, 1, 3, 2, 4).reshape(-1)
+    s = s.reshape(E, NT * 16, KG, 16).permute(0, 2, 1, 3).reshape(-1)
     assert torch.equal(w.q.cpu(), q)
     assert torch.equal(w.s.cpu(), s)
 

@@ -36,12 +36,12 @@ def quantize(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(), w4.OK), (dict(dtype=2), w4.OK), (dict(K=8), w4.OK), (dict(scales=P(4)), w4.OK),
+    (dict(), w4.OK), (dict(dtype=2), w4.OK), (dict(K=8), w4.OK),
     (dict(X=None), w4.ERR_NULL), (dict(codes=None), w4.ERR_NULL), (dict(scales=None), w4.ERR_NULL),
     (dict(dtype=3), w4.ERR_SHAPE), (dict(dtype=-1), w4.ERR_SHAPE), (dict(M=0), w4.ERR_SHAPE),
     (dict(K=0), w4.ERR_SHAPE), (dict(K=12), w4.ERR_SHAPE), (dict(K=(1 << 24) + 8), w4.ERR_SHAPE),
     (dict(M=1 << 31, K=8), w4.ERR_SHAPE), (dict(M=1 << 20, K=1 << 18), w4.ERR_SHAPE),
-    (dict(X=P(8)), w4.ERR_ALIGN), (dict(codes=P(8)), w4.ERR_ALIGN), (dict(scales=P(2)), w4.ERR_ALIGN),
+    (dict(X=P(8)), w4.ERR_ALIGN), (dict(codes=P(8)), w4.ERR_ALIGN), (dict(scales=P(4)), w4.ERR_ALIGN),
 ])
 def test_quantize_args(kw, status):
     assert quantize(**kw) == status
@@ -57,11 +57,11 @@ def weight(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(), w4.OK), (dict(E=1024), w4.OK), (dict(scales=P(4)), w4.OK), (dict(codes=None), w4.ERR_NULL),
+    (dict(), w4.OK), (dict(E=1024), w4.OK), (dict(codes=None), w4.ERR_NULL),
     (dict(s=None), w4.ERR_NULL), (dict(E=0), w4.ERR_SHAPE), (dict(E=1025), w4.ERR_SHAPE), (dict(N=0), w4.ERR_SHAPE),
     (dict(N=1 << 22), w4.ERR_SHAPE), (dict(K=20), w4.ERR_SHAPE), (dict(K=(1 << 20) + 8), w4.ERR_SHAPE),
     (dict(N=1 << 16, K=1 << 16), w4.ERR_SHAPE),     # 2 GiB of codes
-    (dict(q=P(4)), w4.ERR_ALIGN), (dict(codes=P(4)), w4.ERR_ALIGN), (dict(scales=P(1)), w4.ERR_ALIGN),
+    (dict(q=P(4)), w4.ERR_ALIGN), (dict(codes=P(4)), w4.ERR_ALIGN), (dict(scales=P(8)), w4.ERR_ALIGN),
 ])
 def test_weight_args(kw, status):
     assert weight(**kw) == status
@@ -75,17 +75,18 @@ def test_weight_size():
 
 
 def gemm(**kw):
-    a = dict(X=P(), xs=None, xt=0, M=4, K=64, q=P(1 << 33), s=P(1 << 34), N=40, yt=0, Y=P(1 << 32))
+    a = dict(X=P(), xs=None, xt=0, M=4, K=64, q=P(1 << 33), s=P(1 << 34), N=40, yt=0, Y=P(1 << 32), ws=P(1 << 37),
+             wsb=1 << 40)
     a.update(kw)
     return mx._mx().w4a16_mx_check_gemm_args(*a.values())
 
 
 PRODUCT = [
-    (dict(), w4.OK), (dict(xt=1, yt=1), w4.OK), (dict(xs=P(4), xt=0, yt=1), w4.OK),
+    (dict(), w4.OK), (dict(xt=1, yt=1), w4.OK), (dict(xs=P(1 << 31), xt=0, yt=1), w4.OK),
     (dict(X=None), w4.ERR_NULL), (dict(q=None), w4.ERR_NULL), (dict(s=None), w4.ERR_NULL), (dict(Y=None), w4.ERR_NULL),
     (dict(xt=0, yt=1), w4.ERR_SHAPE), (dict(xt=2, yt=2), w4.ERR_SHAPE), (dict(K=4), w4.ERR_SHAPE),
     (dict(N=0), w4.ERR_SHAPE), (dict(X=P(8)), w4.ERR_ALIGN), (dict(Y=P((1 << 32) + 2)), w4.ERR_ALIGN),
-    (dict(xs=P(2)), w4.ERR_ALIGN), (dict(q=P(4)), w4.ERR_ALIGN),
+    (dict(xs=P(8)), w4.ERR_ALIGN), (dict(q=P(4)), w4.ERR_ALIGN),
     (dict(Y=P(256)), w4.ERR_SHAPE),                      # inside X
     (dict(Y=P(), X=P(0x10000), xs=P(0x100)), w4.ERR_SHAPE),   # over the scales
 ]
@@ -117,10 +118,10 @@ def test_grouped_args(kw, status):
 
 def test_the_binding_refuses_what_is_not_on_a_device():
     x = torch.zeros((2, 64), dtype=torch.float16)
-    t = mx.MXTensor(torch.zeros((2, 64), dtype=torch.uint8), torch.zeros((2, 4), dtype=torch.uint8), 64)
+    t = mx.MXTensor(torch.zeros((2, 2, 128), dtype=torch.uint8), torch.zeros((1, 2, 16), dtype=torch.uint8), 64)
     w = mx.MXWeight(torch.zeros(1024, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8), 1, 16, 64)
     for call in (lambda: mx.quantize(x), lambda: mx.dequantize(t), lambda: mx.gemm(x, w), lambda: mx.gemm(t, w),
-                 lambda: mx.tensor(t.codes, t.scales),
+                 lambda: mx.tensor(t.codes, t.codes),
                  lambda: mx.grouped_gemm(x, w, torch.zeros(2, dtype=torch.int32))):
         with pytest.raises(ValueError):
             call()

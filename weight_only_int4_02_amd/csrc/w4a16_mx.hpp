@@ -13,23 +13,30 @@ enum MxX { MX_X_F16 = 0, MX_X_BF16 = 1, MX_X_FP4 = 2 };
 // One product: E matrices, rows sorted by matrix (a plain product has E = 1 and
 // no offsets).
 struct MxArgs {
-    const void *X;            // 16-bit [T][K], or codes [T][64 KT]
-    const uint8_t *xs;        // scales [T][4 KT] (codes only)
+    const void *X;            // 16-bit [T][K], or codes [2 KG][T][128]
+    const uint8_t *xs;        // scales [KG][T][16] (codes only)
     const int32_t *rows;      // [R], or null: row i
     const int32_t *offsets;   // [E + 1], or null
     const void *qd, *sd;      // device layout, matrix 0
     void *Y;                  // [R][N]
+    float *part;              // splits' sums [splits][R][NP] (splits > 1)
     int64_t T, R;
     int E, N, K, KT, NT, KG;
+    int splits, NP;           // NP: N in whole groups of 4
 };
+
+// Output tiles of the large kernel.
+enum MxShape { MX_64x128, MX_64x256, MX_128x128, MX_128x256, MX_256x256 };
 
 struct MxPlan {
     int large;    // the compute-bound kernel
     // small kernel: row tiles of 16, column tiles of 16, waves along K
     int mt, nb, ks;
-    int shape;    // large kernel: output tile
+    int shape;    // large kernel: output tile (MxShape),
+    int splits;   // and workgroups along K
+    size_t ws_bytes;
 };
-MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4);
+MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool grouped);
 
 int launch_mx_quantize(const void *X, int dtype, int64_t M, int64_t K, uint8_t *codes,
                        uint8_t *scales, void *stream);

@@ -22,7 +22,7 @@ int32_t enqueue(const char *what, int32_t st, F launch) {
 int run_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t T, int64_t K,
                 const int32_t *rows, int64_t R, const int32_t *offsets, int64_t E,
                 const void *q_dev, const void *s_dev, int64_t N, int32_t y_dtype, void *Y,
-                void *stream) {
+                void *workspace, void *stream) {
     MxArgs a;
     a.X = X;
     a.xs = x_scales;
@@ -39,7 +39,10 @@ int run_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t
     a.KT = (int)((K + 127) / 128);
     a.NT = (int)((N + 15) / 16);
     a.KG = (a.KT + 3) / 4;
-    const MxPlan p = plan_mx(R, E, N, K, x_scales != nullptr);
+    const MxPlan p = plan_mx(R, E, N, K, x_scales != nullptr, offsets != nullptr);
+    a.part = (float *)workspace;
+    a.splits = p.splits;
+    a.NP = (int)((N + 3) / 4 * 4);
     const int x = x_scales ? MX_X_FP4 : x_dtype == W4A16_MX_BF16 ? MX_X_BF16 : MX_X_F16;
     const bool ybf = y_dtype == W4A16_MX_BF16;
     return p.large ? launch_mx_large(a, p, x, ybf, stream) : launch_mx_small(a, p, x, ybf, stream);
@@ -71,12 +74,14 @@ int32_t w4a16_mx_weight(const uint8_t *codes, const uint8_t *scales, int64_t E, 
 
 int32_t w4a16_mx_gemm(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t M,
                       int64_t K, const void *q_dev, const void *s_dev, int64_t N,
-                      int32_t y_dtype, void *Y, void *stream) {
+                      int32_t y_dtype, void *Y, void *workspace, size_t workspace_bytes,
+                      void *stream) {
     return enqueue("w4a16_mx_gemm",
-                   w4a16_mx_check_gemm_args(X, x_scales, x_dtype, M, K, q_dev, s_dev, N, y_dtype, Y),
+                   w4a16_mx_check_gemm_args(X, x_scales, x_dtype, M, K, q_dev, s_dev, N, y_dtype, Y,
+                                            workspace, workspace_bytes),
                    [&] {
                        return run_product(X, x_scales, x_dtype, M, K, nullptr, M, nullptr, 1, q_dev,
-                                          s_dev, N, y_dtype, Y, stream);
+                                          s_dev, N, y_dtype, Y, workspace, stream);
                    });
 }
 
@@ -89,7 +94,7 @@ int32_t w4a16_mx_grouped_gemm(const void *X, const uint8_t *x_scales, int32_t x_
                                                     q_dev, s_dev, N, y_dtype, Y),
                    [&] {
                        return run_product(X, x_scales, x_dtype, T, K, rows, R, offsets, E, q_dev,
-                                          s_dev, N, y_dtype, Y, stream);
+                                          s_dev, N, y_dtype, Y, nullptr, stream);
                    });
 }
 

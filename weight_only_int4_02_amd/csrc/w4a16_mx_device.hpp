@@ -63,12 +63,16 @@ __device__ __forceinline__ uint32_t mx_pack2(float a, float b) {
         return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2_t{a, b}, h2_t));
 }
 
+__device__ __forceinline__ u2_t mx_pack4(bool bf, float v0, float v1, float v2, float v3) {
+    return bf ? u2_t{mx_pack2<true>(v0, v1), mx_pack2<true>(v2, v3)}
+              : u2_t{mx_pack2<false>(v0, v1), mx_pack2<false>(v2, v3)};
+}
+
 // Four neighbouring results of one row, rounded and stored: columns n .. n + 3
 // of the row at y (of N columns); n is a multiple of 4.
-template <bool BF>
-__device__ __forceinline__ void mx_store4(uint16_t *y, int n, int N, float v0, float v1, float v2,
+__device__ __forceinline__ void mx_store4(uint16_t *y, int n, int N, bool bf, float v0, float v1, float v2,
                                           float v3) {
-    const u2_t v = {mx_pack2<BF>(v0, v1), mx_pack2<BF>(v2, v3)};
+    const u2_t v = mx_pack4(bf, v0, v1, v2, v3);
     if ((N & 3) == 0) {     // (rows are aligned to 8 bytes)
         if (n < N)
             *(u2_t *)(y + n) = v;
@@ -156,6 +160,47 @@ __device__ __forceinline__ MxTile mx_find_tile(const MxArgs &a, int t, int lane)
         }
         before = __builtin_amdgcn_readlane(incl, 63);
     }
+    return out;
+}
+
+// The same from a table in LDS of the tiles up to and with each matrix, made
+// once by one wave.
+template <int BM>
+__device__ __forceinline__ void mx_tile_table(const MxArgs &a, int *table, int lane) {
+    int before = 0;
+    for (int base = 0; base < a.E; base += 64) {
+        const int e = base + lane;
+        int n = 0;
+        if (e < a.E) {
+            const int r = mx_offset(a, e + 1) - mx_offset(a, e);
+            n = r > 0 ? (r + BM - 1) / BM : 0;
+        }
+        const int incl = before + wave_scan(n, lane);
+        if (e < a.E)
+            table[e] = incl;
+        before = __builtin_amdgcn_readlane(incl, 63);
+    }
+}
+
+template <int BM>
+__device__ __forceinline__ MxTile mx_table_tile(const MxArgs &a, const int *table, int t, int lane) {
+    MxTile out = {};
+    for (int base = 0; base < a.E; base += 64) {
+        const int e = base + lane;
+        const uint64_t past = __ballot(e < a.E && table[e < a.E ? e : 0] > t);
+        if (past) {
+            out.e = base + __builtin_ctzll(past);
+            break;
+        }
+    }
+    const int before = __builtin_amdgcn_readfirstlane(out.e ? table[out.e - 1] : 0);
+    out.count = __builtin_amdgcn_readfirstlane(table[out.e]) - before;
+    // (scalar loads: a vector load would wait for the copies under way)
+    const auto *offsets = (const __attribute__((address_space(4))) int *)(uintptr_t)a.offsets;
+    const int R = (int)a.R, o = offsets[out.e], p = offsets[out.e + 1];
+    out.start = o < 0 ? 0 : o > R ? R : o;
+    out.total = (p < 0 ? 0 : p > R ? R : p) - out.start;
+    out.take(t - before, BM);
     return out;
 }
 

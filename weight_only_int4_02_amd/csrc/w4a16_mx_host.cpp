@@ -17,10 +17,11 @@ bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
 }
 
 int64_t ktiles(int64_t K) { return (K + 127) / 128; }
+int64_t kslabs(int64_t K) { return (K + 511) / 512; }
 
 int32_t check_rows(int64_t M, int64_t K, int32_t dtype) {
     if (M <= 0 || M >= (int64_t(1) << 31) || K <= 0 || K > (int64_t(1) << 24) || K % 8 != 0 ||
-        M * ktiles(K) >= (int64_t(1) << 31) || dtype < W4A16_MX_F16 || dtype > W4A16_MX_F32)
+        M * kslabs(K) * 4 >= (int64_t(1) << 31) || dtype < W4A16_MX_F16 || dtype > W4A16_MX_F32)
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
@@ -46,36 +47,83 @@ int32_t check_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, i
         (y_dtype != W4A16_MX_F16 && y_dtype != W4A16_MX_BF16) || (!x_scales && x_dtype != y_dtype))
         return W4A16_ERR_SHAPE;
     // the activations too are addressed with 31-bit byte offsets
-    const int64_t x_bytes = x_scales ? T * ktiles(K) * 64 : T * K * 2;
+    const int64_t x_bytes = x_scales ? T * kslabs(K) * 256 : T * K * 2;
     if (x_bytes >= (int64_t(1) << 31))
         return W4A16_ERR_SHAPE;
     if (!X || !q_dev || !s_dev || !Y)
         return W4A16_ERR_NULL;
     if (!aligned(X, 16) || !aligned(q_dev, 16) || !aligned(s_dev, 16) || !aligned(Y, 16) ||
-        !aligned(x_scales, 4))
+        !aligned(x_scales, 16))
         return W4A16_ERR_ALIGN;
     if (overlap(X, x_bytes, Y, R * N * 2) ||
-        (x_scales && overlap(x_scales, T * ktiles(K) * 4, Y, R * N * 2)))
+        (x_scales && overlap(x_scales, T * kslabs(K) * 16, Y, R * N * 2)))
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
 
 }  // namespace
 
-MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4) {
-    (void)fp4;
+// The large kernel's output tiles: workgroups that share a compute unit, whether K
+// may be split over workgroups, and microseconds a stage (64 columns of 16-bit
+// activations, 256 of MXFP4): `alone`, what a workgroup needs at least (the copies'
+// latency), and `work`, what each adds to a busy compute unit.
+struct MxTileCost {
+    int shape, bm, bn, occ, split;
+    double alone, work;
+};
+const MxTileCost kTiles16[] = {{MX_64x128, 64, 128, 3, 1, 0.40, 0.235}, {MX_64x256, 64, 256, 2, 1, 0.52, 0.41},
+                               {MX_128x128, 128, 128, 2, 1, 0.55, 0.43}, {MX_128x256, 128, 256, 2, 1, 0.92, 0.82},
+                               {MX_256x256, 256, 256, 1, 0, 1.2, 1.62}};
+const MxTileCost kTiles4[] = {{MX_64x128, 64, 128, 2, 1, 0.62, 0.44}, {MX_128x128, 128, 128, 2, 1, 1.0, 0.63},
+                              {MX_128x256, 128, 256, 1, 0, 1.1, 1.1}, {MX_256x256, 256, 256, 1, 0, 1.8, 2.05}};
+
+MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool grouped) {
     MxPlan p = {};
-    const int64_t per = (R + E - 1) / E;   // rows per matrix, on average
+    const int64_t hit = R < E ? R : E;      // matrices with rows, if the rows are spread evenly,
+    const double per = (double)R / (double)hit;   // and the rows of each
     const int64_t nt = (N + 15) / 16, kt = ktiles(K);
-    p.large = per > (E > 1 ? 32 : 64);
-    p.mt = per > 32 ? 4 : per > 16 ? 2 : 1;
-    p.nb = p.mt == 1 ? 1 : 2;
-    // waves along K until the chip has about 16 waves a compute unit
-    const int64_t hit = R < E ? R : E;
-    const int64_t waves = (nt + p.nb - 1) / p.nb * hit;
-    p.ks = 1;
-    while (p.ks < 8 && waves * p.ks < 4096 && p.ks * 4 <= kt)
-        p.ks *= 2;
+    p.splits = 1;
+    // Few rows: the memory-bound kernel.
+    p.large = grouped ? per > 8 : R > 32 || (R > 16 && nt * kt > (fp4 ? 32768 : 16384));
+    if (!p.large) {
+        p.mt = !grouped && R > 16 ? 2 : 1;
+        p.nb = grouped ? 4 : nt <= 384 ? 1 : nt <= 640 ? 2 : 3;
+        // waves along K until the chip has enough in all
+        const int64_t blocks = (nt + p.nb - 1) / p.nb * hit, enough = grouped ? 2300 : 1800;
+        p.ks = 1;
+        while (p.ks < 8 && blocks * p.ks < enough && p.ks * 2 <= kt)
+            p.ks *= 2;
+        return p;
+    }
+    const int64_t stages = fp4 ? (K + 255) / 256 : (K + 63) / 64;
+    const double most_bytes = 512.0 * (1 << 20);   // of splits' sums
+    double best = 1e30;
+    const MxTileCost *tiles = fp4 ? kTiles4 : kTiles16;
+    const int n = fp4 ? 4 : 5;
+    for (int k = 0; k < n; k++) {
+        const MxTileCost &t = tiles[k];
+        // (a matrix's last tile is half full on average)
+        const double rows = grouped ? hit * (per <= t.bm / 2 ? 1.0 : per / t.bm + 0.5) : (double)((R + t.bm - 1) / t.bm);
+        const double items = rows * (double)((N + t.bn - 1) / t.bn);
+        for (int64_t sp = 1; sp <= 16; sp++) {
+            const double sum_bytes = (double)sp * R * N * 8;
+            if (sp > 1 && (grouped || !t.split || sp * 2 > stages || sum_bytes > 2 * most_bytes))
+                break;
+            const double each = (double)((stages + sp - 1) / sp);
+            const double rounds = (int64_t)((items * sp + 256 * t.occ - 1) / (256 * t.occ));
+            const double deep = (int64_t)((items * sp + 255) / 256);
+            const double alone = each * t.alone * rounds, work = each * t.work * deep;
+            double us = 1.5 * rounds + (alone > work ? alone : work);
+            if (sp > 1)
+                us += 2.0 + sum_bytes / 6e6;
+            if (us < best) {
+                best = us;
+                p.shape = t.shape;
+                p.splits = (int)sp;
+            }
+        }
+    }
+    p.ws_bytes = p.splits > 1 ? (size_t)(p.splits * R * ((N + 3) / 4 * 4) * 4) : 0;
     return p;
 }
 
@@ -92,7 +140,7 @@ int32_t w4a16_mx_check_quantize_args(const void *X, int32_t dtype, int64_t M, in
         return st;
     if (!X || !codes || !scales)
         return W4A16_ERR_NULL;
-    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 4))
+    if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 16))
         return W4A16_ERR_ALIGN;
     return W4A16_OK;
 }
@@ -110,7 +158,7 @@ int32_t w4a16_mx_weight_size(int64_t E, int64_t N, int64_t K, size_t *q_bytes, s
         return st;
     const int64_t nt = (N + 15) / 16, kt = ktiles(K);
     *q_bytes = (size_t)(E * nt * kt * 1024);
-    *s_bytes = (size_t)(E * nt * ((kt + 3) / 4) * 256);
+    *s_bytes = (size_t)(E * nt * kslabs(K) * 256);
     return W4A16_OK;
 }
 
@@ -121,15 +169,37 @@ int32_t w4a16_mx_check_weight_args(const uint8_t *codes, const uint8_t *scales, 
         return st;
     if (!codes || !scales || !q_dev || !s_dev)
         return W4A16_ERR_NULL;
-    if (!aligned(codes, 16) || !aligned(scales, 4) || !aligned(q_dev, 16) || !aligned(s_dev, 16))
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(q_dev, 16) || !aligned(s_dev, 16))
         return W4A16_ERR_ALIGN;
     return W4A16_OK;
 }
 
 int32_t w4a16_mx_check_gemm_args(const void *X, const uint8_t *x_scales, int32_t x_dtype,
                                  int64_t M, int64_t K, const void *q_dev, const void *s_dev,
-                                 int64_t N, int32_t y_dtype, const void *Y) {
-    return check_product(X, x_scales, x_dtype, M, K, M, 1, q_dev, s_dev, N, y_dtype, Y);
+                                 int64_t N, int32_t y_dtype, const void *Y,
+                                 const void *workspace, size_t workspace_bytes) {
+    const int32_t st = check_product(X, x_scales, x_dtype, M, K, M, 1, q_dev, s_dev, N, y_dtype, Y);
+    if (st)
+        return st;
+    const size_t need = plan_mx(M, 1, N, K, x_scales != nullptr, false).ws_bytes;
+    if (!need)
+        return W4A16_OK;
+    if (!workspace)
+        return W4A16_ERR_NULL;
+    if (!aligned(workspace, 16))
+        return W4A16_ERR_ALIGN;
+    return workspace_bytes < need ? W4A16_ERR_WORKSPACE : W4A16_OK;
+}
+
+int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantized,
+                                     size_t *bytes) {
+    if (!bytes)
+        return W4A16_ERR_NULL;
+    const int32_t st = check_weight_shape(1, N, K);
+    if (st || M <= 0 || M >= (int64_t(1) << 31))
+        return st ? st : W4A16_ERR_SHAPE;
+    *bytes = plan_mx(M, 1, N, K, quantized != 0, false).ws_bytes;
+    return W4A16_OK;
 }
 
 int32_t w4a16_mx_check_grouped_gemm_args(const void *X, const uint8_t *x_scales, int32_t x_dtype,

@@ -1,13 +1,13 @@
 // Products with MXFP4 weights for many rows (compute-bound).
 //
 // A workgroup's waves form a BM x BN tile of Y, WM x WN of it each, from stages
-// of K in a ring in LDS (128 columns of MXFP4 activations, 64 of 16-bit ones: 64
-// and 128 bytes of a row).  Every wave copies its share of a stage by
+// of K in a ring in LDS: 128 bytes of a row of activations, that is 256 columns
+// of MXFP4 or 64 of a 16-bit type.  Every wave copies its share of a stage by
 // buffer-to-LDS DMA, NBUF - 1 stages ahead of the products; the copies are inline
 // assembly that the compiler does not count, so that it never waits for one by
 // itself.  A stage holds the activation rows (gathered, if an index is given: a
-// lane of a copy has its own address), the weights' 16 x 128 tiles as they lie,
-// and the scale words of both.
+// lane of a copy has its own address) and the weights' 16 x 64 tiles as they lie.  Scales are copied a slab of 512 columns at a time, 16 bytes a
+// row, when the slab's first stage is.
 //
 // Matrix instructions of 32 x 32, the weights first, so that a lane ends with
 // four neighbouring columns of one row.  A lane's operand is 16 bytes, one block of
@@ -17,10 +17,13 @@
 // K are the same eight for both operands.
 //
 // LDS: the weights' 16-byte blocks lie in the order in which lanes read them.  A
-// row of activations is 4 (or 8) blocks of 16 bytes, stored at the block's number
-// XOR a function of the row, so that the lanes of a read (one block of
-// consecutive rows) reach all banks.
+// row of activations is 8 blocks of 16 bytes, stored at the block's number XOR a
+// function of the row, so that the lanes of a read (one block of consecutive
+// rows) reach all banks.  Results leave through LDS too, 32 rows of a wave at a
+// time, so that a store writes whole runs of a row.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "w4a16_mx_device.hpp"
 
@@ -29,212 +32,292 @@ namespace w4a16 {
 namespace {
 
 constexpr int kXcds = 8;  // MI355X: 8 XCDs, workgroups dealt round-robin
+constexpr int kCus = 256;
+constexpr int kMaxMatrices = 1024;
 
-// Copies 16 (4) bytes a lane to LDS at lds + 16 (4) lane; lds is the same in
-// all lanes.  Out of range: zeros.  (M0, which the compiler uses for nothing else
-// in these kernels, holds the address.)
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Copies 16 bytes a lane to LDS at lds + 16 lane; lds is the same in all lanes.
+// Out of range: zeros.  (M0, which the compiler uses for nothing else in these
+// kernels, holds the address.  Its write and the s_nop are the five wait states
+// that the load needs after a vector instruction wrote a scalar register it reads,
+// a spilled one's reload among them.  It names no memory: what it writes is read
+// behind the barrier of a later stage only, and reads of the present stage may be
+// moved past it.)
 __device__ __forceinline__ void copy16(i4_t desc, uint32_t lds, uint32_t voffset, uint32_t soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voffset), "s"(desc), "s"(soffset) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :: "s"(lds), "v"(voffset), "s"(desc), "s"(soffset));
 }
-__device__ __forceinline__ void copy4(i4_t desc, uint32_t lds, uint32_t voffset, uint32_t soffset) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voffset), "s"(desc), "s"(soffset) : "memory");
-}
-
 // Every wave's reads of the stage before are done, and its copies of this one.
 template <int N>
 __device__ __forceinline__ void stage_ready() {
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Where block `b` of row `row` stands among the row's 4 or 8: any 8 or 16
-// consecutive rows' blocks of one number lie in different banks.
-template <bool FP4>
-__device__ __forceinline__ uint32_t swizzle(uint32_t row, uint32_t b) {
-    return FP4 ? b ^ ((row >> 1) & 3) ^ ((row >> 3) & 1) : b ^ (row & 7) ^ ((row >> 3) & 1);
+// Every wave's reads of the last stage are done (and its copies, if ALL).
+template <bool ALL>
+__device__ __forceinline__ void used_up() {
+    if constexpr (ALL)
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    else
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-template <int XT, bool YBF, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool GROUPED>
+// Where block `b` of row `row` stands among the row's 8: any 8 or 16 consecutive
+// rows' blocks of one number lie in different banks.
+__device__ __forceinline__ uint32_t swizzle(uint32_t row, uint32_t b) {
+    return b ^ (row & 7) ^ ((row >> 3) & 1);
+}
+
+// f with 0 .. 3, known when it is compiled.
+template <typename F>
+__device__ __forceinline__ void four(F f) {
+    f(std::integral_constant<int, 0>{});
+    f(std::integral_constant<int, 1>{});
+    f(std::integral_constant<int, 2>{});
+    f(std::integral_constant<int, 3>{});
+}
+
+template <int XT, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY, bool GROUPED>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, OCC * (BM / WM) * (BN / WN) / 4)
-void mx_large_kernel(MxArgs a, int blocks_n) {
+void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     constexpr bool FP4 = XT == MX_X_FP4;
-    constexpr int WAVES_M = BM / WM, WAVES = WAVES_M * (BN / WN);
+    constexpr bool SPLIT = !STAY && !GROUPED;        // K may be split over workgroups
+    constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N;
     constexpr int TM = WM / 32, TN = WN / 32;
-    constexpr int XROW = FP4 ? 64 : 128;             // bytes of a stage's row
-    constexpr int XCH = BM * XROW / 1024;            // copies of a stage: activations,
-    constexpr int WCH = BN * (FP4 ? 64 : 32) / 1024; // weights,
-    constexpr int SW = BN / 64, SX = FP4 ? BM / 64 : 0;   // scale words
+    constexpr int XROW = 128;                        // bytes of a stage's row
+    constexpr int SPS = FP4 ? 2 : 8;                 // stages of a slab
+    constexpr int XCH = BM / 8;                      // copies of 1 KiB of a stage: activations,
+    constexpr int WCH = FP4 ? BN / 8 : BN / 32;      // weights;
+    constexpr int SX = FP4 ? BM / 64 : 0, SCH = BN / 64 + SX;   // of a slab: scales
     static_assert(XCH % WAVES == 0 && WCH % WAVES == 0, "copies split evenly over the waves");
-    constexpr int KX = XCH / WAVES, KW = WCH / WAVES, KSC = (SW + SX + WAVES - 1) / WAVES;
-    constexpr int CPW = KX + KW + KSC;               // copies of a wave and stage
-    static_assert((NBUF - 1) * CPW < 64, "counted by vmcnt");
-    constexpr int STAGE = (XCH + WCH) * 1024 + KSC * WAVES * 256;
-    __shared__ __attribute__((aligned(1024))) char lds[NBUF * STAGE];
+    constexpr int KX = XCH / WAVES, KW = WCH / WAVES, KSC = (SCH + WAVES - 1) / WAVES;
+    constexpr int CPW = KX + KW;                     // copies of a wave and stage
+    static_assert((NBUF - 1) * (CPW + KSC) < 64, "counted by vmcnt");
+    constexpr int STAGE = (XCH + WCH) * 1024, SLAB = KSC * WAVES * 1024;
+    // slabs that the stages of the ring can belong to (of one tile; of tiles of one stage)
+    constexpr int NSLAB = STAY ? NBUF : (NBUF - 2) / SPS + 2;
+    constexpr int OUT = 32 * (WN > 64 ? WN : 64) * 2;    // a wave's results on their way
+    static_assert(WAVES * OUT <= (STAY ? 1 : NBUF) * STAGE, "they pass through the ring's stages that are free");
+    constexpr int TABLE = STAY && GROUPED ? kMaxMatrices * 4 : 0;
+    __shared__ __attribute__((aligned(1024))) char lds[NBUF * STAGE + NSLAB * SLAB + TABLE];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave % WAVES_M, wn = wave / WAVES_M;
+    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int h = lane >> 5, l32 = lane & 31;
 
-    // this workgroup's tile: the XCDs take equal runs of them, column block by
-    // column block of a matrix, its row tiles one after the other, so that
-    // neighbours in time share the weights of a column block in their L2
-    const uint32_t xcd = blockIdx.x % kXcds, at = blockIdx.x / kXcds;
+    // this workgroup's tiles (one, unless STAY): the XCDs take equal runs of them,
+    // column block by column block of a matrix, its row tiles one after the other,
+    // so that neighbours in time share the weights of a column block in their L2
+    const uint32_t xcd = blockIdx.x % kXcds, wg = blockIdx.x / kXcds, wgs = gridDim.x / kXcds;
+    int *const table = (int *)(lds + NBUF * STAGE + NSLAB * SLAB);   // tiles up to each matrix
     uint32_t tiles;
-    if constexpr (GROUPED)
-        tiles = (uint32_t)mx_count_tiles<BM>(a, lane);
-    else
+    if constexpr (!GROUPED) {
         tiles = (uint32_t)((a.R + BM - 1) / BM);
-    const uint32_t items = tiles * (uint32_t)blocks_n;
-    const uint32_t first = items / kXcds * xcd + min(items % kXcds, xcd);
-    if (at >= items / kXcds + (items % kXcds > xcd ? 1 : 0))
-        return;
-    const uint32_t item = first + at;
-    MxTile t;
-    int nb;
-    if constexpr (GROUPED) {
-        const uint32_t any = item / (uint32_t)blocks_n;
-        t = mx_find_tile<BM>(a, (int)any, lane);
-        if (t.count == 0)
-            return;
-        // (within the matrix: column block, then row tile)
-        const uint32_t within = item - (any - (uint32_t)t.mt) * (uint32_t)blocks_n;
-        nb = (int)(within / (uint32_t)t.count);
-        t.take((int)(within - (uint32_t)nb * (uint32_t)t.count), BM);
+    } else if constexpr (STAY) {
+        if (wave == 0)
+            mx_tile_table<BM>(a, table, lane);
+        __syncthreads();
+        tiles = (uint32_t)__builtin_amdgcn_readfirstlane(table[a.E - 1]);
     } else {
-        nb = (int)(item / tiles);
-        t = MxTile{0, 0, (int)a.R, (int)tiles};
-        t.take((int)(item - (uint32_t)nb * tiles), BM);
+        tiles = (uint32_t)mx_count_tiles<BM>(a, lane);
     }
+    const uint32_t whole = tiles * (uint32_t)blocks_n, items = SPLIT ? whole * (uint32_t)a.splits : whole;
+    const uint32_t first = items / kXcds * xcd + min(items % kXcds, xcd);
+    const uint32_t run = items / kXcds + (items % kXcds > xcd ? 1 : 0);
+    const uint32_t mine = (uint32_t)uniform(run > wg ? (int)((run - wg + wgs - 1) / wgs) : 0);
+    if (mine == 0)
+        return;
+    struct Item {
+        MxTile t;
+        int nb, split;
+    };
+    auto find = [&](uint32_t k) __attribute__((always_inline)) {
+        Item it;
+        const uint32_t at = first + wg + k * wgs;
+        it.split = SPLIT ? uniform((int)(at / whole)) : 0;
+        const uint32_t item = at - (uint32_t)it.split * whole;
+        if constexpr (GROUPED) {
+            const uint32_t any = (uint32_t)uniform((int)(item / (uint32_t)blocks_n));
+            it.t = STAY ? mx_table_tile<BM>(a, table, (int)any, lane) : mx_find_tile<BM>(a, (int)any, lane);
+            // (within the matrix: column block, then row tile)
+            const uint32_t within = item - (any - (uint32_t)it.t.mt) * (uint32_t)blocks_n;
+            it.nb = uniform((int)(within / (uint32_t)it.t.count));
+            it.t.take((int)(within - (uint32_t)it.nb * (uint32_t)it.t.count), BM);
+        } else {
+            it.nb = uniform((int)(item / tiles));
+            it.t = MxTile{0, 0, (int)a.R, (int)tiles};
+            it.t.take((int)(item - (uint32_t)it.nb * tiles), BM);
+        }
+        return it;
+    };
 
     const uint32_t wbytes = (uint32_t)a.NT * (uint32_t)a.KT * 1024u, sbytes = (uint32_t)a.NT * (uint32_t)a.KG * 256u;
-    const i4_t dw = make_desc((const char *)a.qd + (int64_t)t.e * wbytes, wbytes);
-    const i4_t ds = make_desc((const char *)a.sd + (int64_t)t.e * sbytes, sbytes);
-    const uint32_t xrow = FP4 ? (uint32_t)a.KT * 64u : (uint32_t)a.K * 2u;
-    const i4_t dx = make_desc(a.X, (uint32_t)(a.T * xrow));
-    const i4_t dxs = make_desc(a.xs, FP4 ? (uint32_t)(a.T * a.KT * 4) : 0u);
+    const uint32_t xrow = FP4 ? 128u : (uint32_t)a.K * 2u;
+    const i4_t dx = make_desc(a.X, (uint32_t)(a.T * (FP4 ? a.KG * 256 : a.K * 2)));
+    const i4_t dxs = make_desc(a.xs, FP4 ? (uint32_t)(a.T * a.KG * 16) : 0u);
 
-    // the copies' per-lane offsets
-    auto source_row = [&](int i) __attribute__((always_inline)) {
+    // The rows of X that a lane copies in a tile, as the index has them: of 8 a copy,
+    // and of 64 a copy of scales.  (They are looked at when the tile's copies begin:
+    // until then they may be on their way.)
+    struct Rows {
+        uint32_t x[KX], s[KSC];
+    };
+    auto source_row = [&](const MxTile &t, int i) __attribute__((always_inline)) {
         uint32_t row = (uint32_t)(t.row0 + i);
         if (GROUPED && a.rows)
             row = i < t.rows ? (uint32_t)a.rows[t.row0 + i] : ~0u;
-        return i < t.rows && row < (uint32_t)a.T ? row : ~0u;
+        return i < t.rows ? row : ~0u;
     };
-    constexpr int RPC = 1024 / XROW;     // rows of an activation copy
-    constexpr int LPR = 64 / RPC;        // and lanes of a row
-    uint32_t xo[KX], xcol = 0, wo[KW], so[KSC];
-#pragma unroll
-    for (int k = 0; k < KX; k++) {
-        const int i = (wave + k * WAVES) * RPC + lane / LPR;
-        const uint32_t row = source_row(i), b = swizzle<FP4>((uint32_t)i, (uint32_t)(lane % LPR));
-        xo[k] = row != ~0u ? row * xrow + 16u * b : kOutOfRange;
-        // (8 columns a block of 16-bit activations; the same for every k: the
-        // copies are 32 rows apart or more, and the order goes by the row's number below 16)
-        static_assert(WAVES * RPC % 16 == 0, "a lane's copies have one order of blocks");
-        xcol = 8u * b;
-    }
-    const int nt0 = nb * (BN / 16);
-#pragma unroll
-    for (int k = 0; k < KW; k++) {
-        // FP4: one tile a copy; else the same half of two
-        const int c = wave + k * WAVES;
-        const int nt = nt0 + (FP4 ? c : 2 * c + (lane >> 5));
-        wo[k] = nt < a.NT ? (uint32_t)nt * (uint32_t)a.KT * 1024u + 16u * (FP4 ? lane : lane & 31) : kOutOfRange;
-    }
-#pragma unroll
-    for (int k = 0; k < KSC; k++) {
-        // 64 columns' (or rows') words a copy
-        const int c = wave + k * WAVES;
-        const int nt = nt0 + 4 * c + (lane >> 4);
-        so[k] = kOutOfRange;
-        if (c < SW) {
-            if (nt < a.NT)
-                so[k] = (uint32_t)nt * (uint32_t)a.KG * 256u + 16u * (lane & 15);
-        } else if (FP4 && c < SW + SX) {
-            const uint32_t row = source_row((c - SW) * 64 + lane);
-            if (row != ~0u)
-                so[k] = row * (uint32_t)a.KT * 4u;
-        }
-    }
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
-    const int stages = FP4 ? a.KT : (a.K + 63) / 64;
-    auto issue = [&](int s, int buf) __attribute__((always_inline)) {
-        const uint32_t to = lds0 + (uint32_t)(buf * STAGE);
-        const int kt = FP4 ? s : s >> 1;
+    auto source_rows = [&](const MxTile &t) __attribute__((always_inline)) {
+        Rows r;
 #pragma unroll
         for (int k = 0; k < KX; k++)
-            copy16(dx, to + (uint32_t)(wave + k * WAVES) * 1024u,
-                   FP4 || (int)xcol < a.K - s * 64 ? xo[k] : kOutOfRange, (uint32_t)(s * XROW));
+            r.x[k] = source_row(t, (wave + k * WAVES) * 8 + lane / 8);
 #pragma unroll
-        for (int k = 0; k < KW; k++)
-            copy16(dw, to + (uint32_t)(XCH + wave + k * WAVES) * 1024u, wo[k],
-                   (uint32_t)kt * 1024u + (FP4 ? 0u : 512u * (s & 1)));
+        for (int k = 0; k < KSC; k++) {
+            const int c = wave + k * WAVES - BN / 64;
+            r.s[k] = FP4 && c >= 0 && c < SX ? source_row(t, c * 64 + lane) : ~0u;
+        }
+        return r;
+    };
+    // A lane's block of an activation row is the same in all of a wave's copies
+    // (they are 16 rows apart or a multiple, and the order of blocks goes by the
+    // row's number below 16).
+    static_assert(WAVES % 2 == 0, "a lane's copies have one order of blocks");
+    const uint32_t xblock = swizzle((uint32_t)(wave * 8 + lane / 8), (uint32_t)(lane % 8));
+    // the tile whose stages are being copied, and its copies' offsets
+    i4_t dw, ds;
+    uint32_t xo[KX], so[KSC];
+    int nt0;
+    auto begin = [&](const Item &it, const Rows &rows) __attribute__((always_inline)) {
+        dw = make_desc((const char *)a.qd + (int64_t)it.t.e * wbytes, wbytes);
+        ds = make_desc((const char *)a.sd + (int64_t)it.t.e * sbytes, sbytes);
+#pragma unroll
+        for (int k = 0; k < KX; k++)
+            xo[k] = rows.x[k] < (uint32_t)a.T ? rows.x[k] * xrow + 16u * xblock : kOutOfRange;
+        nt0 = it.nb * (BN / 16);
+#pragma unroll
+        for (int k = 0; k < KSC; k++) {
+            // the scales of 64 columns (or rows) a copy
+            const int c = wave + k * WAVES;
+            so[k] = kOutOfRange;
+            if (c < BN / 64) {
+                const int nt = nt0 + 4 * c + (lane >> 4);
+                if (nt < a.NT)
+                    so[k] = (uint32_t)nt * 256u + 16u * (lane & 15);
+            } else if (rows.s[k] < (uint32_t)a.T) {
+                so[k] = rows.s[k] * 16u;
+            }
+        }
+    };
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
+    // the stages of a split
+    const int all = FP4 ? (a.K + 255) / 256 : (a.K + 63) / 64;
+    auto stage_from = [&](int split) __attribute__((always_inline)) {
+        return SPLIT ? uniform(all * split / a.splits) : split * all;
+    };
+    // the copies of stage s of the current tile: the scales of its slab, to `place`,
+    auto issue_slab = [&](int s, int place) __attribute__((always_inline)) {
+        const uint32_t slab = (uint32_t)(s / SPS);
+        const uint32_t at = lds0 + (uint32_t)(NBUF * STAGE + place * SLAB);
 #pragma unroll
         for (int k = 0; k < KSC; k++) {
             const int c = wave + k * WAVES;
-            const uint32_t l = to + (uint32_t)(XCH + WCH) * 1024u + (uint32_t)c * 256u;
-            if (!FP4 || c < SW)
-                copy4(ds, l, so[k], (uint32_t)(kt >> 2) * 256u + 4u * (uint32_t)(kt & 3));
+            if (!FP4 || c < BN / 64)
+                copy16(ds, at + 1024u * (uint32_t)c, so[k], slab * (uint32_t)a.NT * 256u);
             else
-                copy4(dxs, l, so[k], 4u * (uint32_t)kt);
+                copy16(dxs, at + 1024u * (uint32_t)c, so[k], slab * (uint32_t)a.T * 16u);
+        }
+    };
+    // and copies k0 .. k1 - 1 of the wave's CPW: activations, then weights, two tiles'
+    // 64 columns a copy, 1 KiB as they lie.  (Past the last tile of rows the last one
+    // again, whose results nobody stores; past the last of K zeros.)
+    auto issue = [&](int s, int buf, uint32_t none, auto k0_c, auto k1_c) __attribute__((always_inline)) {
+        constexpr int k0 = decltype(k0_c)::value, k1 = decltype(k1_c)::value;
+        const uint32_t to = lds0 + (uint32_t)(buf * STAGE);
+#pragma unroll
+        for (int k = k0; k < (k1 < KX ? k1 : KX); k++)
+            copy16(dx, to + (uint32_t)(wave + k * WAVES) * 1024u,
+                   none | (FP4 || (int)(8 * xblock) < a.K - s * 64 ? xo[k] : kOutOfRange),
+                   FP4 ? (uint32_t)s * (uint32_t)a.T * 128u : (uint32_t)(s * XROW));
+#pragma unroll
+        for (int k = (k0 > KX ? k0 - KX : 0); k < k1 - KX; k++) {
+            const int c = wave + k * WAVES;
+            const int kq = FP4 ? 4 * s + c / (BN / 32) : s, two = nt0 + 2 * (c % (BN / 32));
+            const int nt = two < a.NT ? two : a.NT - 1;
+            const bool in = !none && (!FP4 || kq < 2 * a.KT);
+            copy16(dw, to + (uint32_t)(XCH + c) * 1024u,
+                   in ? 16u * (nt + 1 < a.NT ? lane : lane & 31) : kOutOfRange,
+                   in ? (uint32_t)(kq * a.NT + nt) * 512u : 0u);
         }
     };
 
     f16_t acc[TM][TN];
-#pragma unroll
-    for (int m = 0; m < TM; m++)
-#pragma unroll
-        for (int n = 0; n < TN; n++)
-#pragma unroll
-            for (int i = 0; i < 16; i++)
-                acc[m][n][i] = 0.f;
-
-    auto compute = [&](int s, int buf) __attribute__((always_inline)) {
+    // stage s; `between` is called in each of its four parts
+    auto compute = [&](int s, int buf, int place, auto between) __attribute__((always_inline)) {
         const char *st = lds + buf * STAGE;
         const char *x = st + (wm * WM + l32) * XROW;
-        const char *w = st + XCH * 1024 + (wn * (WN / 16) + (l32 >> 4)) * (FP4 ? 1024 : 512) + h * 256 + (l32 & 15) * 16;
-        const uint32_t *sw = (const uint32_t *)(st + (XCH + WCH) * 1024) + wn * WN + l32;
-        const uint32_t *sx = (const uint32_t *)(st + (XCH + WCH) * 1024) + SW * 64 + wm * WM + l32;
+        const char *w = st + XCH * 1024 + (wn * (WN / 16) + (l32 >> 4)) * 512 + h * 256 + (l32 & 15) * 16;
+        const char *slab = lds + NBUF * STAGE + place * SLAB;
+        const char *sw = slab + (wn * WN + l32) * 16, *sx = slab + (BN + wm * WM + l32) * 16;
         if constexpr (FP4) {
-            uint32_t xs[TM], ws[TN];
+            // of a row's two scale words of the stage, the lane's blocks in bytes 0 and 2
+            u2_t xs[TM], ws[TN];
 #pragma unroll
             for (int m = 0; m < TM; m++)
-                xs[m] = sx[32 * m] >> (8 * h);
+                xs[m] = *(const u2_t *)(sx + 512 * m + 8 * (s & 1)) >> (uint32_t)(8 * h);
 #pragma unroll
             for (int n = 0; n < TN; n++)
-                ws[n] = sw[32 * n] >> (8 * h);
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                u4_t xa[TM], wa[TN];
+                ws[n] = *(const u2_t *)(sw + 512 * n + 8 * (s & 1)) >> (uint32_t)(8 * h);
+            u4_t xa[2][TM], wa[2][TN];        // (the next 64 columns are read during these)
+            auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
                 for (int m = 0; m < TM; m++)
-                    xa[m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle<true>((uint32_t)l32, (uint32_t)(2 * j + h)));
+                    xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle((uint32_t)l32, (uint32_t)(2 * j + h)));
 #pragma unroll
                 for (int n = 0; n < TN; n++)
-                    wa[n] = *(const u4_t *)(w + n * 2048 + j * 512);
+                    wa[j & 1][n] = *(const u4_t *)(w + n * 1024 + j * (BN * 32));
+            };
+            read(0);
+            four([&](auto jc) __attribute__((always_inline)) {     // 64 columns each
+                constexpr int j = decltype(jc)::value;
+                if (j < 3)
+                    read(j + 1);
 #pragma unroll
-                for (int n = 0; n < TN; n++)
+                for (int n = 0; n < TN; n++) {
 #pragma unroll
                     for (int m = 0; m < TM; m++)
-                        acc[m][n] = j == 0 ? mx_mfma32<0>(wa[n], xa[m], acc[m][n], ws[n], xs[m])
-                                           : mx_mfma32<2>(wa[n], xa[m], acc[m][n], ws[n], xs[m]);
-            }
+                        acc[m][n] = j % 2 == 0
+                            ? mx_mfma32<0>(wa[j & 1][n], xa[j & 1][m], acc[m][n], ws[n][j / 2], xs[m][j / 2])
+                            : mx_mfma32<2>(wa[j & 1][n], xa[j & 1][m], acc[m][n], ws[n][j / 2], xs[m][j / 2]);
+                    if (n == 0)
+                        between(jc);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
         } else {
             float ws[TN];
             u4_t wa[TN];
 #pragma unroll
             for (int n = 0; n < TN; n++) {
-                ws[n] = mx_scale(sw[32 * n], (uint32_t)(2 * (s & 1) + h));
+                // (the slab's scale of block 2 s + h)
+                ws[n] = __builtin_bit_cast(float, (uint32_t)*(const uint8_t *)(sw + 512 * n + 2 * (s % SPS) + h) << 23);
                 wa[n] = *(const u4_t *)(w + n * 1024);
             }
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                u4_t xa[TM];
+            u4_t xa[2][TM];
+            auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
                 for (int m = 0; m < TM; m++)
-                    xa[m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle<false>((uint32_t)l32, (uint32_t)(4 * h + j)));
+                    xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle((uint32_t)l32, (uint32_t)(4 * h + j)));
+            };
+            read(0);
+            four([&](auto jc) __attribute__((always_inline)) {
+                constexpr int j = decltype(jc)::value;
+                if (j < 3)
+                    read(j + 1);
 #pragma unroll
                 for (int n = 0; n < TN; n++) {
                     const u4_t v = mx_decode<XT == MX_X_BF16>(wa[n][j], ws[n]);
@@ -242,70 +325,242 @@ void mx_large_kernel(MxArgs a, int blocks_n) {
                     for (int m = 0; m < TM; m++) {
                         if constexpr (XT == MX_X_BF16)
                             acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                                __builtin_bit_cast(bf8_t, v), __builtin_bit_cast(bf8_t, xa[m]), acc[m][n], 0, 0, 0);
+                                __builtin_bit_cast(bf8_t, v), __builtin_bit_cast(bf8_t, xa[j & 1][m]), acc[m][n], 0, 0, 0);
                         else
                             acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-                                __builtin_bit_cast(h8_t, v), __builtin_bit_cast(h8_t, xa[m]), acc[m][n], 0, 0, 0);
+                                __builtin_bit_cast(h8_t, v), __builtin_bit_cast(h8_t, xa[j & 1][m]), acc[m][n], 0, 0, 0);
                     }
+                    if (n == 0)
+                        between(jc);
                 }
-            }
+                __builtin_amdgcn_sched_barrier(0);
+            });
         }
     };
 
+    // The stages of all tiles are one stream.  The copies run NBUF - 1 stages ahead,
+    // into the next tile while this one's results are stored: `i` has the place of
+    // the copies, `next` what the tile after theirs needs.
+    struct {
+        int s, s1, buf, place;
+        uint32_t k;
+    } i;
+    Item now = find(0), next = now;
+    Rows rows = source_rows(now.t);
+    uint32_t known = 0;                 // the tile that `next` and `rows` are of
+    begin(now, rows);
+    i = {stage_from(now.split), stage_from(now.split + 1), 0, 0, 0};
+    bool fresh = true;                  // i.s is its tile's first
+    auto look_ahead = [&]() __attribute__((always_inline)) {
+        if (STAY && known == i.k && i.k + 1 < mine) {
+            known = i.k + 1;
+            next = find(known);
+            if constexpr (GROUPED)
+                rows = source_rows(next.t);
+        }
+    };
+    // goes on to the next stage to copy, its tile's offsets and its slab; whether
+    // there is one
+    auto next_stage = [&]() __attribute__((always_inline)) {
+        if (i.s == i.s1) {
+            if (!STAY || i.k + 1 >= mine)
+                return false;
+            look_ahead();
+            i.k++;
+            if constexpr (GROUPED)
+                begin(next, rows);
+            else
+                begin(next, source_rows(next.t));
+            i.s = stage_from(next.split);
+            i.s1 = stage_from(next.split + 1);
+            fresh = true;
+        }
+        if (fresh || i.s % SPS == 0) {
+            i.place = i.place + 1 < NSLAB ? i.place + 1 : 0;
+            issue_slab(i.s, i.place);
+        }
+        fresh = false;
+        return true;
+    };
 #pragma unroll
-    for (int s = 0; s < NBUF - 1; s++)
-        if (s < stages)
-            issue(s, s);
-    int buf = 0;
-    for (int s = 0; s < stages; s++) {
-        // (copies of the NBUF - 2 stages after this one may be under way)
-        if (s + NBUF - 2 < stages)
-            stage_ready<(NBUF - 2) * CPW>();
-        else
-            stage_ready<0>();
-        if (s + NBUF - 1 < stages)
-            issue(s + NBUF - 1, buf == 0 ? NBUF - 1 : buf - 1);
-        compute(s, buf);
-        buf = buf + 1 < NBUF ? buf + 1 : 0;
+    for (int k = 0; k < NBUF - 1; k++) {
+        const uint32_t none = next_stage() ? 0u : kOutOfRange;
+        issue(i.s, i.buf, none, std::integral_constant<int, 0>{}, std::integral_constant<int, CPW>{});
+        i.s += none ? 0 : 1;
+        i.buf = i.buf + 1 < NBUF ? i.buf + 1 : 0;
     }
+    int buf = 0, place = 0;
+    for (uint32_t k = 0; k < mine; k++) {
+        const int s0 = stage_from(now.split), s1 = stage_from(now.split + 1);
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+            for (int n = 0; n < TN; n++)
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    acc[m][n][e] = 0.f;
+        for (int s = s0; s < s1; s++) {
+            // (copies of the NBUF - 2 stages after this one may be under way)
+            stage_ready<(NBUF - 2) * CPW>();
+            // (Behind the last stage of all, copies of nothing: zeros, read by nobody.)
+            const uint32_t none = next_stage() ? 0u : kOutOfRange;
+            if (s == s0)
+                look_ahead();
+            if (s == s0 || s % SPS == 0)
+                place = place + 1 < NSLAB ? place + 1 : 0;
+            if constexpr (NBUF == 2) {
+                // the copies have to land within this stage: all at once
+                issue(i.s, i.buf, none, std::integral_constant<int, 0>{}, std::integral_constant<int, CPW>{});
+                compute(s, buf, place, [](auto) {});
+            } else {
+                // a quarter at a time between the products: all at once they fill the
+                // memory pipeline's queue and hold the waves up (2048 x 22016 x 4096 in
+                // bf16 293 -> 288 us)
+                compute(s, buf, place, [&](auto j) __attribute__((always_inline)) {
+                    constexpr int at = decltype(j)::value;
+                    issue(i.s, i.buf, none, std::integral_constant<int, CPW * at / 4>{},
+                          std::integral_constant<int, CPW * (at + 1) / 4>{});
+                });
+            }
+            i.s += none ? 0 : 1;
+            i.buf = i.buf + 1 < NBUF ? i.buf + 1 : 0;
+            buf = buf + 1 < NBUF ? buf + 1 : 0;
+        }
+        // the results, 32 rows of the wave's at a time through its part of the stage
+        // just used (the next copy there is issued after the next stage's barrier)
+        used_up<!STAY>();
+        const MxTile t = now.t;
+        const int split = now.split, n0 = now.nb * BN + wn * WN;
+        char *out = lds + (STAY ? (buf == 0 ? NBUF - 1 : buf - 1) * STAGE : 0) + wave * OUT;
+#pragma unroll
+        for (int m = 0; m < TM; m++) {
+            const int i0 = wm * WM + 32 * m;
+            if (i0 >= t.rows)
+                break;
+            const int rows_here = t.rows - i0 < 32 ? t.rows - i0 : 32;
+            if (SPLIT && a.splits > 1) {
+                // fp32 sums of this split (rows of whole groups of four columns), 32
+                // columns at a time
+                float *part = a.part + ((int64_t)split * a.R + t.row0 + i0) * a.NP + n0;
+                const int g = lane % 8;
+#pragma unroll
+                for (int n = 0; n < TN; n++) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        *(f4_t *)(out + l32 * 128 + 16 * ((2 * q + h) ^ (l32 & 7))) =
+                            f4_t{acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]};
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const int r = 8 * k + lane / 8;
+                        const f4_t v = *(const f4_t *)(out + r * 128 + 16 * (g ^ (r & 7)));
+                        if (r < rows_here && n0 + 32 * n + 4 * g < a.N)
+                            *(f4_t *)(part + (int64_t)r * a.NP + 32 * n + 4 * g) = v;
+                    }
+                }
+                continue;
+            }
+            constexpr int G = WN / 8, X = G < 8 ? G - 1 : 7;
+            const bool bf = FP4 ? ybf : XT == MX_X_BF16;
+#pragma unroll
+            for (int n = 0; n < TN; n++)
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    *(u2_t *)(out + l32 * (WN * 2) + 16 * ((4 * n + q) ^ (l32 & X)) + 8 * h) =
+                        mx_pack4(bf, acc[m][n][4 * q], acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
+            uint16_t *y = (uint16_t *)a.Y + (int64_t)(t.row0 + i0) * a.N + n0;
+            // (a row of Y starts at a multiple of 16, 4 or 2 bytes)
+            if ((a.N & 7) == 0) {
+                const int g = lane % G;
+#pragma unroll
+                for (int k = 0; k < 32 * G / 64; k++) {
+                    const int r = k * (64 / G) + lane / G;
+                    const u4_t v = *(const u4_t *)(out + r * (WN * 2) + 16 * (g ^ (r & X)));
+                    if (r < rows_here && n0 + 8 * g < a.N)
+                        *(u4_t *)(y + (int64_t)r * a.N + 8 * g) = v;
+                }
+            } else if ((a.N & 1) == 0) {
+                constexpr int P = WN / 2;                // pairs of columns a row
+                const int c = 2 * (lane % P);
+                for (int r = lane / P; r < rows_here; r += 64 / P)
+                    if (n0 + c < a.N)
+                        *(uint32_t *)(y + (int64_t)r * a.N + c) =
+                            *(const uint32_t *)(out + r * (WN * 2) + 16 * ((c >> 3) ^ (r & X)) + 2 * (c & 7));
+            } else {
+                for (int at = lane; at < rows_here * WN; at += 64) {
+                    const int r = at / WN, c = at % WN;
+                    if (n0 + c < a.N)
+                        y[(int64_t)r * a.N + c] =
+                            *(const uint16_t *)(out + r * (WN * 2) + 16 * ((c >> 3) ^ (r & X)) + 2 * (c & 7));
+                }
+            }
+        }
+        if constexpr (!STAY)
+            return;
+        if (k + 1 < mine)
+            now = find(k + 1);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // (copies of nothing: the LDS is still ours)
+}
 
-#pragma unroll
-    for (int m = 0; m < TM; m++) {
-        const int i = wm * WM + 32 * m + l32;
-        if (i >= t.rows)
-            continue;
-        uint16_t *y = (uint16_t *)a.Y + (int64_t)(t.row0 + i) * a.N;
-#pragma unroll
-        for (int n = 0; n < TN; n++)
-#pragma unroll
-            for (int q = 0; q < 4; q++)
-                mx_store4<YBF>(y, nb * BN + wn * WN + 32 * n + 8 * q + 4 * h, a.N, acc[m][n][4 * q],
-                               acc[m][n][4 * q + 1], acc[m][n][4 * q + 2], acc[m][n][4 * q + 3]);
+// The splits' sums, in their order, rounded: four columns a thread.
+constexpr int kSumThreads = 256;
+__global__ __launch_bounds__(kSumThreads) void mx_sum_kernel(MxArgs a, int64_t groups, bool ybf) {
+    const int per = a.NP / 4;
+    for (int64_t i = (int64_t)blockIdx.x * kSumThreads + threadIdx.x; i < groups;
+         i += (int64_t)gridDim.x * kSumThreads) {
+        const int64_t row = i / per;
+        const int n = (int)(i - row * per) * 4;
+        f4_t v = *(const f4_t *)(a.part + 4 * i);
+        for (int k = 1; k < a.splits; k++)
+            v += *(const f4_t *)(a.part + (int64_t)k * a.R * a.NP + 4 * i);
+        mx_store4((uint16_t *)a.Y + row * a.N, n, a.N, ybf, v[0], v[1], v[2], v[3]);
     }
 }
 
-template <int XT, bool YBF, int BM, int BN, int WM, int WN, int NBUF, int OCC>
-int launch_inst(const MxArgs &a, hipStream_t st) {
+template <int XT, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY>
+int launch_inst(const MxArgs &a, bool ybf, hipStream_t st) {
     const int64_t blocks = (a.N + BN - 1) / BN;
     const int64_t used = a.R < a.E ? a.R : a.E;
     const int64_t tiles = a.offsets ? used + (a.R - used) / BM : (a.R + BM - 1) / BM;
-    const int64_t grid = (tiles * blocks + kXcds - 1) / kXcds * kXcds;
+    const int64_t items = tiles * blocks * a.splits, most = STAY && items > kCus ? kCus : items;
+    const int64_t grid = (most + kXcds - 1) / kXcds * kXcds;
     constexpr int threads = (BM / WM) * (BN / WN) * 64;
-    if (grid * threads >= (int64_t(1) << 32))
+    if (items >= (int64_t(1) << 31) || grid * threads >= (int64_t(1) << 32))
         return (int)hipErrorInvalidConfiguration;
-    if (a.offsets)
-        hipLaunchKernelGGL((mx_large_kernel<XT, YBF, BM, BN, WM, WN, NBUF, OCC, true>), dim3((unsigned)grid),
-                           dim3(threads), 0, st, a, (int)blocks);
-    else
-        hipLaunchKernelGGL((mx_large_kernel<XT, YBF, BM, BN, WM, WN, NBUF, OCC, false>), dim3((unsigned)grid),
-                           dim3(threads), 0, st, a, (int)blocks);
+    if (a.offsets) {
+        hipLaunchKernelGGL((mx_large_kernel<XT, BM, BN, WM, WN, NBUF, OCC, STAY, true>), dim3((unsigned)grid),
+                           dim3(threads), 0, st, a, (int)blocks, ybf);
+        return (int)hipGetLastError();
+    }
+    hipLaunchKernelGGL((mx_large_kernel<XT, BM, BN, WM, WN, NBUF, OCC, STAY, false>), dim3((unsigned)grid),
+                       dim3(threads), 0, st, a, (int)blocks, ybf);
+    const int e = (int)hipGetLastError();
+    if (e || a.splits == 1)
+        return e;
+    const int64_t groups = a.R * (a.NP / 4), wgs = (groups + kSumThreads - 1) / kSumThreads;
+    hipLaunchKernelGGL(mx_sum_kernel, dim3((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20)), dim3(kSumThreads), 0, st, a, groups,
+                       XT == MX_X_FP4 ? ybf : XT == MX_X_BF16);
     return (int)hipGetLastError();
 }
 
-template <int XT, bool YBF>
-int launch_shape(const MxArgs &a, const MxPlan &p, hipStream_t st) {
-    (void)p;
-    return launch_inst<XT, YBF, 128, 256, 64, 128, 3, 2>(a, st);
+template <int XT>
+int launch_shape(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
+    constexpr bool FP4 = XT == MX_X_FP4;
+    switch (p.shape) {
+    case MX_64x128: return launch_inst<XT, 64, 128, 32, 64, 3, FP4 ? 2 : 3, false>(a, ybf, st);
+    case MX_64x256:
+        if constexpr (!FP4)     // (plan_mx: never the cheapest)
+            return launch_inst<XT, 64, 256, 64, 64, 4, 2, false>(a, ybf, st);
+        break;
+    case MX_128x128: return launch_inst<XT, 128, 128, 64, 64, FP4 ? 2 : 3, 2, false>(a, ybf, st);
+    case MX_128x256:
+        if constexpr (FP4)
+            return launch_inst<XT, 128, 256, 64, 64, 2, 1, true>(a, ybf, st);
+        else
+            return launch_inst<XT, 128, 256, 128, 64, 3, 2, false>(a, ybf, st);
+    default: break;
+    }
+    return launch_inst<XT, 256, 256, 128, 64, FP4 ? 2 : 3, 1, true>(a, ybf, st);
 }
 
 }  // namespace
@@ -313,10 +568,10 @@ int launch_shape(const MxArgs &a, const MxPlan &p, hipStream_t st) {
 int launch_mx_large(const MxArgs &a, const MxPlan &p, int x, bool ybf, void *stream) {
     hipStream_t st = (hipStream_t)stream;
     if (x == MX_X_F16)
-        return launch_shape<MX_X_F16, false>(a, p, st);
+        return launch_shape<MX_X_F16>(a, p, ybf, st);
     if (x == MX_X_BF16)
-        return launch_shape<MX_X_BF16, true>(a, p, st);
-    return ybf ? launch_shape<MX_X_FP4, true>(a, p, st) : launch_shape<MX_X_FP4, false>(a, p, st);
+        return launch_shape<MX_X_BF16>(a, p, ybf, st);
+    return launch_shape<MX_X_FP4>(a, p, ybf, st);
 }
 
 }  // namespace w4a16

@@ -3,8 +3,8 @@
 // A workgroup takes NB column tiles of 16 and MT row tiles of 16, its KS waves
 // (or, of one wave along K, four workgroups' worth of columns side by side)
 // each every KS-th 128-column tile of K.  A weight tile is one 16-byte load a
-// lane, straight into the operand registers: the device layout is the lanes'
-// order, block 4 of a row in lanes 16 b + r.  The weights are the first operand, so a lane
+// lane, straight into the operand registers (block b of row r in lane 16 b + r).
+// The weights are the first operand, so a lane
 // holds four neighbouring columns of one row's results.  With 16-bit
 // activations, word j of a lane's block multiplies the same eight columns of its
 // row of X, a matrix instruction of 16 x 16 x 32 for each j: the order of K
@@ -24,6 +24,16 @@ __device__ __forceinline__ uint32_t load4(__amdgpu_buffer_rsrc_t r, uint32_t v, 
     return (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(r, (int)v, (int)s, 0);
 }
 
+// Words j of the four lane groups become group j's four words: in lanes 16 i + r
+// word j is then word i of block j.
+__device__ __forceinline__ u4_t transpose_words(u4_t w) {
+    const auto a = __builtin_amdgcn_permlane16_swap(w.x, w.y, false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(w.z, w.w, false, false);
+    const auto c = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+    return u4_t{c[0], d[0], c[1], d[1]};
+}
+
 // One 128-column tile's operands of a wave.
 template <int XT, int MT, int NB>
 struct Stage {
@@ -32,11 +42,13 @@ struct Stage {
 };
 
 // WAVES: of the workgroup; KS of them along K, the others on further columns.
-template <int XT, bool YBF, int MT, int NB, int WAVES, int KS, int DEPTH, bool GROUPED>
-__global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int blocks_n) {
+template <int XT, int MT, int NB, int WAVES, int KS, int DEPTH, bool GROUPED>
+__global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int blocks_n, bool ybf) {
     constexpr bool FP4 = XT == MX_X_FP4;
     constexpr int NW = WAVES / KS;
-    __shared__ f4_t sums[KS > 1 ? WAVES * MT * NB * 64 : 1];
+    // column tiles whose sums lie in LDS at a time (at most 64 KiB)
+    constexpr int NP = WAVES * MT * NB <= 64 ? NB : 64 / (WAVES * MT);
+    __shared__ f4_t sums[KS > 1 ? WAVES * MT * NP * 64 : 1];
     const int lane = threadIdx.x & 63, r = lane & 15, kb = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int ks = wave % KS, nw = wave / KS;
@@ -57,9 +69,10 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
     const uint32_t wbytes = (uint32_t)a.NT * (uint32_t)a.KT * 1024u, sbytes = (uint32_t)a.NT * (uint32_t)a.KG * 256u;
     const __amdgpu_buffer_rsrc_t rw = make_rsrc((const char *)a.qd + (int64_t)t.e * wbytes, wbytes);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc((const char *)a.sd + (int64_t)t.e * sbytes, sbytes);
-    const uint32_t xrow = FP4 ? (uint32_t)a.KT * 64u : (uint32_t)a.K * 2u;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, (uint32_t)(a.T * xrow));
-    const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs, FP4 ? (uint32_t)(a.T * a.KT * 4) : 0u);
+    const uint32_t xrow = FP4 ? 128u : (uint32_t)a.K * 2u;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(a.X, (uint32_t)(a.T * (FP4 ? a.KG * 256 : a.K * 2)));
+    const __amdgpu_buffer_rsrc_t rxs = make_rsrc(a.xs, FP4 ? (uint32_t)(a.T * a.KG * 16) : 0u);
+    const uint32_t wo = (uint32_t)(kb >> 1) * (uint32_t)a.NT * 512u + 256u * (kb & 1) + 16u * r;
     uint32_t xo[MT], xso[MT];
 #pragma unroll
     for (int m = 0; m < MT; m++) {
@@ -68,8 +81,8 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
         if (GROUPED && a.rows)
             row = i < t.rows ? (uint32_t)a.rows[t.row0 + i] : ~0u;
         const bool in = i < t.rows && row < (uint32_t)a.T;
-        xo[m] = in ? row * xrow + (FP4 ? 16u * kb : 64u * kb) : kOutOfRange;
-        xso[m] = in ? row * (uint32_t)a.KT * 4u : kOutOfRange;
+        xo[m] = in ? row * xrow + 16u * kb : kOutOfRange;
+        xso[m] = in ? row * 16u : kOutOfRange;
     }
 
     f4_t acc[MT][NB];
@@ -85,20 +98,21 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
 #pragma unroll
         for (int n = 0; n < NB; n++) {
             const bool here = in && nt0 + n < a.NT;
-            s.w[n] = load16(rw, here ? 16u * lane : kOutOfRange, here ? (uint32_t)((nt0 + n) * a.KT + kt) * 1024u : 0u);
+            s.w[n] = load16(rw, here ? wo : kOutOfRange, here ? (uint32_t)(2 * kt * a.NT + nt0 + n) * 512u : 0u);
             s.ws[n] = load4(rs, here ? 16u * r : kOutOfRange,
-                            here ? (uint32_t)((nt0 + n) * a.KG + (kt >> 2)) * 256u + 4u * (kt & 3) : 0u);
+                            here ? (uint32_t)((kt >> 2) * a.NT + nt0 + n) * 256u + 4u * (kt & 3) : 0u);
         }
 #pragma unroll
         for (int m = 0; m < MT; m++) {
             if constexpr (FP4) {
-                s.x[m][0] = load16(rx, in ? xo[m] : kOutOfRange, in ? 64u * kt : 0u);
-                s.xs[m] = load4(rxs, in ? xso[m] : kOutOfRange, in ? 4u * kt : 0u);
+                s.x[m][0] = load16(rx, in ? xo[m] : kOutOfRange, in ? (uint32_t)(kt >> 1) * (uint32_t)a.T * 128u + 64u * (kt & 1) : 0u);
+                s.xs[m] = load4(rxs, in ? xso[m] : kOutOfRange,
+                                in ? (uint32_t)(kt >> 2) * (uint32_t)a.T * 16u + 4u * (kt & 3) : 0u);
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; j++)
-                    s.x[m][j] = load16(rx, kt * 128 + 32 * kb + 8 * j < a.K ? xo[m] : kOutOfRange,
-                                       in ? 256u * kt + 16u * j : 0u);
+                    s.x[m][j] = load16(rx, kt * 128 + 32 * j + 8 * kb < a.K ? xo[m] : kOutOfRange,
+                                       in ? 256u * kt + 64u * j : 0u);
             }
         }
     };
@@ -118,10 +132,10 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
         } else {
 #pragma unroll
             for (int n = 0; n < NB; n++) {
-                const float ws = mx_scale(s.ws[n], kb);
+                const u4_t words = transpose_words(s.w[n]);
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const u4_t w = mx_decode<XT == MX_X_BF16>(s.w[n][j], ws);
+                    const u4_t w = mx_decode<XT == MX_X_BF16>(words[j], mx_scale(s.ws[n], j));
 #pragma unroll
                     for (int m = 0; m < MT; m++) {
                         if constexpr (XT == MX_X_BF16)
@@ -149,27 +163,34 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
     // the waves' sums, added in their order; tile (m, n) by wave (m NB + n) mod KS
     const auto store = [&](int m, int n, f4_t v) __attribute__((always_inline)) {
         if (16 * m + r < t.rows)
-            mx_store4<YBF>((uint16_t *)a.Y + (int64_t)(t.row0 + 16 * m + r) * a.N, (nt0 + n) * 16 + 4 * kb,
-                           a.N, v[0], v[1], v[2], v[3]);
+            mx_store4((uint16_t *)a.Y + (int64_t)(t.row0 + 16 * m + r) * a.N, (nt0 + n) * 16 + 4 * kb, a.N,
+                      FP4 ? ybf : XT == MX_X_BF16, v[0], v[1], v[2], v[3]);
     };
     if constexpr (KS > 1) {
+        // (NP column tiles a pass)
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+        for (int n0 = 0; n0 < NB; n0 += NP) {
+            if (n0)
+                __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NB; n++)
-                sums[((nw * MT * NB + m * NB + n) * KS + ks) * 64 + lane] = acc[m][n];
-        __syncthreads();
+            for (int m = 0; m < MT; m++)
 #pragma unroll
-        for (int m = 0; m < MT; m++)
+                for (int n = n0; n < n0 + NP && n < NB; n++)
+                    sums[((nw * MT * NP + m * NP + n - n0) * KS + ks) * 64 + lane] = acc[m][n];
+            __syncthreads();
 #pragma unroll
-            for (int n = 0; n < NB; n++)
-                if ((m * NB + n) % KS == ks) {
-                    f4_t v = sums[((nw * MT * NB + m * NB + n) * KS) * 64 + lane];
+            for (int m = 0; m < MT; m++)
 #pragma unroll
-                    for (int k = 1; k < KS; k++)
-                        v += sums[((nw * MT * NB + m * NB + n) * KS + k) * 64 + lane];
-                    store(m, n, v);
-                }
+                for (int n = n0; n < n0 + NP && n < NB; n++)
+                    if ((m * NP + n - n0) % KS == ks) {
+                        const f4_t *from = &sums[(nw * MT * NP + m * NP + n - n0) * KS * 64 + lane];
+                        f4_t v = from[0];
+#pragma unroll
+                        for (int k = 1; k < KS; k++)
+                            v += from[64 * k];
+                        store(m, n, v);
+                    }
+        }
     } else {
 #pragma unroll
         for (int m = 0; m < MT; m++)
@@ -179,44 +200,52 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
     }
 }
 
-template <int XT, bool YBF, int MT, int NB, int WAVES, int KS, bool GROUPED>
-int launch_inst(const MxArgs &a, hipStream_t st) {
-    constexpr int cols = NB * (WAVES / KS), DEPTH = MT == 4 && XT != MX_X_FP4 ? 2 : 4;
+template <int XT, int MT, int NB, int WAVES, int KS, int DEPTH, bool GROUPED>
+int launch_inst(const MxArgs &a, bool ybf, hipStream_t st) {
+    constexpr int cols = NB * (WAVES / KS);
     const int64_t blocks = (a.NT + cols - 1) / cols;
     // sum over the matrices with rows of ceil(rows / (16 MT)), at most
     const int64_t used = a.R < a.E ? a.R : a.E;
     const int64_t tiles = GROUPED ? used + (a.R - used) / (16 * MT) : (a.R + 16 * MT - 1) / (16 * MT);
     if (tiles * blocks * WAVES * 64 >= (int64_t(1) << 32))
         return (int)hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((mx_small_kernel<XT, YBF, MT, NB, WAVES, KS, DEPTH, GROUPED>),
-                       dim3((unsigned)(tiles * blocks)), dim3(WAVES * 64), 0, st, a, (int)blocks);
+    hipLaunchKernelGGL((mx_small_kernel<XT, MT, NB, WAVES, KS, DEPTH, GROUPED>),
+                       dim3((unsigned)(tiles * blocks)), dim3(WAVES * 64), 0, st, a, (int)blocks, ybf);
     return (int)hipGetLastError();
 }
 
-template <int XT, bool YBF, int MT, int NB>
-int launch_ks(const MxArgs &a, const MxPlan &p, hipStream_t st) {
-    if (a.offsets) {
-        switch (p.ks) {
-        case 1: return launch_inst<XT, YBF, MT, NB, 4, 1, true>(a, st);
-        case 2: return launch_inst<XT, YBF, MT, NB, 4, 2, true>(a, st);
-        case 4: return launch_inst<XT, YBF, MT, NB, 4, 4, true>(a, st);
-        default: return launch_inst<XT, YBF, MT, NB, 8, 8, true>(a, st);
-        }
-    }
+template <int XT, int MT, int NB, int DEPTH>
+int launch_ks(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
+    if constexpr (MT == 1)      // (plan_mx: one row tile for matrices of few rows each)
+        if (a.offsets)
+            switch (p.ks) {
+            case 1: return launch_inst<XT, MT, NB, 4, 1, DEPTH, true>(a, ybf, st);
+            case 2: return launch_inst<XT, MT, NB, 4, 2, DEPTH, true>(a, ybf, st);
+            case 4: return launch_inst<XT, MT, NB, 4, 4, DEPTH, true>(a, ybf, st);
+            default: return launch_inst<XT, MT, NB, 8, 8, DEPTH, true>(a, ybf, st);
+            }
     switch (p.ks) {
-    case 1: return launch_inst<XT, YBF, MT, NB, 4, 1, false>(a, st);
-    case 2: return launch_inst<XT, YBF, MT, NB, 4, 2, false>(a, st);
-    case 4: return launch_inst<XT, YBF, MT, NB, 4, 4, false>(a, st);
-    default: return launch_inst<XT, YBF, MT, NB, 8, 8, false>(a, st);
+    case 1: return launch_inst<XT, MT, NB, 4, 1, DEPTH, false>(a, ybf, st);
+    case 2: return launch_inst<XT, MT, NB, 4, 2, DEPTH, false>(a, ybf, st);
+    case 4: return launch_inst<XT, MT, NB, 4, 4, DEPTH, false>(a, ybf, st);
+    default: return launch_inst<XT, MT, NB, 8, 8, DEPTH, false>(a, ybf, st);
     }
 }
 
-template <int XT, bool YBF>
-int launch_mt(const MxArgs &a, const MxPlan &p, hipStream_t st) {
-    switch (p.mt) {
-    case 1: return launch_ks<XT, YBF, 1, 1>(a, p, st);
-    case 2: return launch_ks<XT, YBF, 2, 2>(a, p, st);
-    default: return launch_ks<XT, YBF, 4, 2>(a, p, st);
+template <int XT>
+int launch_mt(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
+    constexpr bool FP4 = XT == MX_X_FP4;
+    if (p.mt == 2)
+        switch (p.nb) {
+        case 1: return launch_ks<XT, 2, 1, 4>(a, p, ybf, st);
+        case 2: return launch_ks<XT, 2, 2, FP4 ? 4 : 3>(a, p, ybf, st);
+        default: return launch_ks<XT, 2, 3, FP4 ? 4 : 3>(a, p, ybf, st);
+        }
+    switch (p.nb) {
+    case 1: return launch_ks<XT, 1, 1, 4>(a, p, ybf, st);
+    case 2: return launch_ks<XT, 1, 2, 4>(a, p, ybf, st);
+    case 3: return launch_ks<XT, 1, 3, 4>(a, p, ybf, st);
+    default: return launch_ks<XT, 1, 4, FP4 ? 4 : 3>(a, p, ybf, st);
     }
 }
 
@@ -225,10 +254,10 @@ int launch_mt(const MxArgs &a, const MxPlan &p, hipStream_t st) {
 int launch_mx_small(const MxArgs &a, const MxPlan &p, int x, bool ybf, void *stream) {
     hipStream_t st = (hipStream_t)stream;
     if (x == MX_X_F16)
-        return launch_mt<MX_X_F16, false>(a, p, st);
+        return launch_mt<MX_X_F16>(a, p, ybf, st);
     if (x == MX_X_BF16)
-        return launch_mt<MX_X_BF16, true>(a, p, st);
-    return ybf ? launch_mt<MX_X_FP4, true>(a, p, st) : launch_mt<MX_X_FP4, false>(a, p, st);
+        return launch_mt<MX_X_BF16>(a, p, ybf, st);
+    return launch_mt<MX_X_FP4>(a, p, ybf, st);
 }
 
 }  // namespace w4a16

@@ -32,7 +32,8 @@ MAX_EXPERTS = 1024
 # Symbols of include/w4a16_mx.h.
 EXPORTS = ("w4a16_mx_quantize", "w4a16_mx_check_quantize_args", "w4a16_mx_dequantize",
            "w4a16_mx_check_dequantize_args", "w4a16_mx_weight_size", "w4a16_mx_weight",
-           "w4a16_mx_check_weight_args", "w4a16_mx_gemm", "w4a16_mx_check_gemm_args",
+           "w4a16_mx_check_weight_args", "w4a16_mx_gemm_workspace_size", "w4a16_mx_gemm",
+           "w4a16_mx_check_gemm_args",
            "w4a16_mx_grouped_gemm", "w4a16_mx_check_grouped_gemm_args")
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
@@ -48,11 +49,12 @@ def _mx():
         P, I64, I32, PSZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)
         args = {"quantize": [P, I32, I64, I64, P, P], "dequantize": [P, P, I64, I64, I32, P],
                 "weight": [P, P, I64, I64, I64, P, P],
-                "gemm": [P, P, I32, I64, I64, P, P, I64, I32, P],
+                "gemm": [P, P, I32, I64, I64, P, P, I64, I32, P, P, ctypes.c_size_t],
                 "grouped_gemm": [P, P, I32, I64, I64, P, I64, P, I64, P, P, I64, I32, P]}
         for name, types in args.items():
             getattr(L, f"w4a16_mx_{name}").argtypes = types + [P]
             getattr(L, f"w4a16_mx_check_{name}_args").argtypes = types
+        L.w4a16_mx_gemm_workspace_size.argtypes = [I64, I64, I64, I32, PSZ]
         L.w4a16_mx_weight_size.argtypes = [I64, I64, I64, PSZ, PSZ]
         for name in EXPORTS:
             getattr(L, name).restype = I32
@@ -62,10 +64,11 @@ def _mx():
 
 @dataclass
 class MXTensor:
-    """MXFP4 rows, owned by torch tensors: codes uint8 [.., 64 KT] (two columns a
-    byte, the first in the low half) and scales uint8 [.., 4 KT] (2^(b - 127), 255
-    for NaN), KT = ceil(K / 128); columns from K on hold zeros.  dtype: the type
-    dequantize() and products give where none is named."""
+    """MXFP4 rows, owned by torch tensors: codes uint8 [2 KG, .., 128] (of 256
+    columns the 128 bytes of each row, two columns a byte, the first in the low half)
+    and scales uint8 [KG, .., 16] (of 512 columns the 16 scales of each row:
+    2^(b - 127), 255 for NaN), KG = ceil(K / 512); columns from K on hold zeros.  dtype: the type dequantize() gives where none is named,
+    and products too (bf16 for fp32)."""
     codes: torch.Tensor
     scales: torch.Tensor
     K: int
@@ -73,7 +76,7 @@ class MXTensor:
 
     @property
     def shape(self):
-        return (*self.codes.shape[:-1], self.K)
+        return (*self.codes.shape[1:-1], self.K)
 
 
 @dataclass
@@ -86,8 +89,8 @@ class MXWeight:
     K: int
 
 
-def _tiles(K: int) -> int:
-    return -(-K // 128)
+def _slabs(K: int) -> int:
+    return -(-K // 512)
 
 
 def _float_type(dtype, types, name: str) -> int:
@@ -97,17 +100,16 @@ def _float_type(dtype, types, name: str) -> int:
 
 
 def _check_tensor(t, name: str, device: int, ndim: Optional[int] = None) -> None:
-    """The tensors of an MXTensor hold what its shape needs (the kernels read
-    them through bare pointers)."""
+    """The tensors of an MXTensor (of ndim dimensions) hold what its shape needs (the
+    kernels read them through bare pointers)."""
     if not isinstance(t, MXTensor):
         raise TypeError(f"{name} must be an MXTensor")
-    ndim = t.codes.dim() if ndim is None else ndim
+    ndim = t.codes.dim() if ndim is None else ndim + 1
     check(t.codes, f"{name}.codes", torch.uint8, ndim, device)
     check(t.scales, f"{name}.scales", torch.uint8, ndim, device)
-    KT = _tiles(t.K)
-    if (t.codes.shape[:-1] != t.scales.shape[:-1] or t.codes.shape[-1] != 64 * KT
-            or t.scales.shape[-1] != 4 * KT):
-        raise ValueError(f"{name}: codes must be [.., {64 * KT}] and scales [.., {4 * KT}] for K = {t.K}, "
+    KG = _slabs(t.K)
+    if ndim < 2 or t.codes.shape != (2 * KG, *t.scales.shape[1:-1], 128) or t.scales.shape[::ndim - 1] != (KG, 16):
+        raise ValueError(f"{name}: codes must be [{2 * KG}, .., 128] and scales [{KG}, .., 16] for K = {t.K}, "
                          f"got {tuple(t.codes.shape)} and {tuple(t.scales.shape)}")
 
 
@@ -129,13 +131,13 @@ def quantize(x: torch.Tensor) -> MXTensor:
     K = x.shape[-1]
     if K < 1 or K % 8:
         raise ValueError("K must be a positive multiple of 8")
-    M, KT = x.numel() // K, _tiles(K)
-    codes = torch.empty((*x.shape[:-1], 64 * KT), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((*x.shape[:-1], 4 * KT), dtype=torch.uint8, device=x.device)
+    M, KG = x.numel() // K, _slabs(K)
+    codes = torch.empty((2 * KG, *x.shape[:-1], 128), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((KG, *x.shape[:-1], 16), dtype=torch.uint8, device=x.device)
     if M:
         _raise(_mx().w4a16_mx_quantize(x.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr(), stream),
                "w4a16_mx_quantize")
-    return MXTensor(codes, scales, K, torch.bfloat16 if x.dtype == torch.float32 else x.dtype)
+    return MXTensor(codes, scales, K, x.dtype)
 
 
 def dequantize(t: MXTensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
@@ -161,25 +163,27 @@ def dequantize(t: MXTensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor
 def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
            dtype: torch.dtype = torch.bfloat16) -> MXTensor:
     """codes uint8 [.., K/2] and scales uint8 [.., ceil(K/32)], as checkpoints hold
-    them, on the device -> MXTensor (padded to whole tiles of 128 columns).  K:
+    them, on the device -> MXTensor (padded to whole slabs of 512 columns).  K:
     twice the codes' last dimension if None."""
     if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() < 1:
         raise ValueError("codes must be a device tensor of at least one dimension")
     device = codes.get_device()
     check(codes, "codes", torch.uint8, codes.dim(), device)
     check(scales, "scales", torch.uint8, codes.dim(), device)
-    _float_type(dtype, (torch.float16, torch.bfloat16), "dtype")
+    _float_type(dtype, tuple(_DTYPES), "dtype")
     K = 2 * codes.shape[-1] if K is None else K
     if K < 1 or K % 8:
         raise ValueError("K must be a positive multiple of 8")
     if (codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != K // 2
             or scales.shape[-1] != -(-K // BLOCK)):
         raise ValueError("codes must be [.., K/2] and scales [.., ceil(K/32)]")
-    KT = _tiles(K)
-    if codes.shape[-1] != 64 * KT:
-        codes = torch.nn.functional.pad(codes, (0, 64 * KT - codes.shape[-1]))
-    if scales.shape[-1] != 4 * KT:
-        scales = torch.nn.functional.pad(scales, (0, 4 * KT - scales.shape[-1]), value=127)
+    KG = _slabs(K)
+    if codes.shape[-1] != 256 * KG:
+        codes = torch.nn.functional.pad(codes, (0, 256 * KG - codes.shape[-1]))
+    if scales.shape[-1] != 16 * KG:
+        scales = torch.nn.functional.pad(scales, (0, 16 * KG - scales.shape[-1]), value=127)
+    codes = codes.unflatten(-1, (2 * KG, 128)).movedim(-2, 0).contiguous()
+    scales = scales.unflatten(-1, (KG, 16)).movedim(-2, 0).contiguous()
     return MXTensor(codes, scales, K, dtype)
 
 
@@ -193,12 +197,12 @@ def weight(t: MXTensor) -> MXWeight:
     """An MXTensor [N, K], or [E, N, K] for E experts, in the products' layout."""
     if not isinstance(t, MXTensor):
         raise TypeError("t must be an MXTensor")
-    if t.codes.dim() not in (2, 3):
+    if t.codes.dim() not in (3, 4):
         raise ValueError("t must be [N, K] or [E, N, K]")
     device = t.codes.get_device()
     _check_tensor(t, "t", device)
     stream = stream_of(device)
-    E, N = (1, *t.codes.shape[:-1]) if t.codes.dim() == 2 else t.codes.shape[:-1]
+    E, N = (1, *t.shape[:-1]) if t.codes.dim() == 3 else t.shape[:-1]
     qb, sb = weight_size(E, N, t.K)
     codes, scales = (x if x.data_ptr() % 16 == 0 else x.clone() for x in (t.codes, t.scales))
     q = torch.empty(qb, dtype=torch.uint8, device=codes.device)
@@ -213,8 +217,8 @@ def _check_weight(w: MXWeight, device: int) -> None:
         raise TypeError("w must be an MXWeight")
     check(w.q, "w.q", torch.uint8, 1, device)
     check(w.s, "w.s", torch.uint8, 1, device)
-    nt, kt = -(-w.N // 16), _tiles(w.K)
-    if w.q.numel() < w.E * nt * kt * 1024 or w.s.numel() < w.E * nt * -(-kt // 4) * 256:
+    nt = w.E * -(-w.N // 16)
+    if w.q.numel() < nt * -(-w.K // 128) * 1024 or w.s.numel() < nt * _slabs(w.K) * 256:
         raise ValueError("MXWeight tensors are smaller than its shape needs")
 
 
@@ -223,7 +227,8 @@ def _activations(x, K: int, dtype):
     if isinstance(x, MXTensor):
         device = x.codes.get_device()
         _check_tensor(x, "x", device, 2)
-        dtype = x.dtype if dtype is None else dtype
+        if dtype is None:
+            dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
         data, scales, xt = x.codes, x.scales, 0
     else:
         if not isinstance(x, torch.Tensor):
@@ -241,19 +246,29 @@ def _activations(x, K: int, dtype):
     return device, data, scales, xt, _float_type(dtype, (torch.float16, torch.bfloat16), "dtype"), dtype
 
 
-def gemm(x, w: MXWeight, out: Optional[torch.Tensor] = None,
-         dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+def gemm_workspace_size(M: int, N: int, K: int, quantized: bool) -> int:
+    b = ctypes.c_size_t()
+    _raise(_mx().w4a16_mx_gemm_workspace_size(M, N, K, quantized, ctypes.byref(b)), "w4a16_mx_gemm_workspace_size")
+    return b.value
+
+
+def gemm(x, w: MXWeight, out: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None,
+         workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y [M, N] = x [M, K] . dequantize(w)^T, with fp32 sums.
 
     x: fp16 or bf16, whose type Y has; the weights enter as their values in
     that type (in fp16: subnormal below 2^-14, infinite from 65520 on).  Or an
-    MXTensor: both operands enter as they are, and Y has `dtype` (x.dtype if
-    None).  M may be 0."""
+    MXTensor: both operands enter as they are, and Y has `dtype` (if None,
+    x.dtype, of an fp32 one bf16).  M may be 0.
+
+    workspace: at least gemm_workspace_size() bytes, for callers that manage
+    their own; without one, a call that needs it takes a new block of torch's
+    allocator (so calls on other streams, and captured ones, have their own)."""
     device, data, scales, xt, yt, dtype = _activations(x, w.K, dtype)
     _check_weight(w, device)
     if w.E != 1:
         raise ValueError("a weight of several experts goes to grouped_gemm")
-    M = data.shape[0]
+    M = x.shape[0]
     if out is None:
         out = torch.empty((M, w.N), dtype=dtype, device=data.device)
     else:
@@ -262,8 +277,14 @@ def gemm(x, w: MXWeight, out: Optional[torch.Tensor] = None,
             raise ValueError("out must be [M, N]")
     stream = stream_of(device)
     if M:
+        need = gemm_workspace_size(M, w.N, w.K, scales is not None)
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=data.device) if need else None
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the call's device")
+        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
         _raise(_mx().w4a16_mx_gemm(data.data_ptr(), None if scales is None else scales.data_ptr(), xt, M, w.K,
-                                   w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(), stream),
+                                   w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(), ws, wsb, stream),
                "w4a16_mx_gemm")
     return out
 
@@ -282,7 +303,7 @@ def grouped_gemm(x, w: MXWeight, offsets: torch.Tensor, rows: Optional[torch.Ten
     check(offsets, "offsets", torch.int32, 1, device)
     if offsets.shape[0] != w.E + 1:
         raise ValueError("offsets must be [E + 1]")
-    T = R = data.shape[0]
+    T = R = x.shape[0]
     if rows is not None:
         check(rows, "rows", torch.int32, 1, device)
         R = rows.shape[0]
