@@ -18,6 +18,7 @@ gradients are formed.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
@@ -37,6 +38,7 @@ EXPORTS = ("w4a16_mx_quantize", "w4a16_mx_check_quantize_args", "w4a16_mx_dequan
            "w4a16_mx_grouped_gemm", "w4a16_mx_check_grouped_gemm_args")
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_DTYPES16 = {torch.float16: 0, torch.bfloat16: 1}
 
 _bound = None
 
@@ -89,28 +91,37 @@ class MXWeight:
     K: int
 
 
-def _slabs(K: int) -> int:
-    return -(-K // 512)
-
-
 def _float_type(dtype, types, name: str) -> int:
-    if dtype not in _DTYPES or dtype not in types:
+    if dtype not in types:
         raise TypeError(f"{name} must be one of {', '.join(str(t) for t in types)}, got {dtype}")
-    return _DTYPES[dtype]
+    return types[dtype]
 
 
-def _check_tensor(t, name: str, device: int, ndim: Optional[int] = None) -> None:
-    """The tensors of an MXTensor (of ndim dimensions) hold what its shape needs (the
-    kernels read them through bare pointers)."""
-    if not isinstance(t, MXTensor):
-        raise TypeError(f"{name} must be an MXTensor")
-    ndim = t.codes.dim() if ndim is None else ndim + 1
-    check(t.codes, f"{name}.codes", torch.uint8, ndim, device)
-    check(t.scales, f"{name}.scales", torch.uint8, ndim, device)
-    KG = _slabs(t.K)
-    if ndim < 2 or t.codes.shape != (2 * KG, *t.scales.shape[1:-1], 128) or t.scales.shape[::ndim - 1] != (KG, 16):
+def _type_of(x, types, name: str) -> int:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return _float_type(x.dtype, types, name)
+
+
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{name} must be on a device")
+    return device
+
+
+def _check_tensor(t: MXTensor, name: str, device: int, rank: int) -> None:
+    """The tensors of an MXTensor of `rank` dimensions hold what its shape needs
+    (the kernels read them through bare pointers)."""
+    codes, scales, KG = t.codes, t.scales, -(-t.K // 512)
+    check(codes, name, torch.uint8, rank + 1, device)
+    check(scales, name, torch.uint8, rank + 1, device)
+    c, s = codes.shape, scales.shape
+    if rank < 1 or c[0] != 2 * KG or s[0] != KG or c[-1] != 128 or s[-1] != 16 or c[1:-1] != s[1:-1]:
         raise ValueError(f"{name}: codes must be [{2 * KG}, .., 128] and scales [{KG}, .., 16] for K = {t.K}, "
-                         f"got {tuple(t.codes.shape)} and {tuple(t.scales.shape)}")
+                         f"got {tuple(c)} and {tuple(s)}")
 
 
 def quantize(x: torch.Tensor) -> MXTensor:
@@ -120,20 +131,18 @@ def quantize(x: torch.Tensor) -> MXTensor:
     elements are rounded to nearest, ties to even, beyond 6 scales to 6.  A block
     that holds an infinity or a NaN becomes NaN throughout.  There may be no
     rows; the last block of a row may be partial."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError("x must be a torch.Tensor")
-    dt = _float_type(x.dtype, tuple(_DTYPES), "x")
-    if x.dim() < 1 or not x.is_cuda:
-        raise ValueError("x must be a device tensor of at least one dimension")
-    device = x.get_device()
-    check(x, "x", x.dtype, x.dim(), device)
-    stream = stream_of(device)
-    K = x.shape[-1]
+    dt = _type_of(x, _DTYPES, "x")
+    device = _device_of(x, "x")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    *rows, K = x.shape or (0,)
     if K < 1 or K % 8:
         raise ValueError("K must be a positive multiple of 8")
-    M, KG = x.numel() // K, _slabs(K)
-    codes = torch.empty((2 * KG, *x.shape[:-1], 128), dtype=torch.uint8, device=x.device)
-    scales = torch.empty((KG, *x.shape[:-1], 16), dtype=torch.uint8, device=x.device)
+    stream = stream_of(device)
+    KG = -(-K // 512)
+    codes = torch.empty((2 * KG, *rows, 128), dtype=torch.uint8, device=x.device)
+    scales = codes.new_empty((KG, *rows, 16))
+    M = x.numel() // K
     if M:
         _raise(_mx().w4a16_mx_quantize(x.data_ptr(), dt, M, K, codes.data_ptr(), scales.data_ptr(), stream),
                "w4a16_mx_quantize")
@@ -145,12 +154,10 @@ def dequantize(t: MXTensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor
     exact in bf16 and fp32, but for magnitudes past the type's largest."""
     if not isinstance(t, MXTensor):
         raise TypeError("t must be an MXTensor")
-    if not t.codes.is_cuda:
-        raise ValueError("t must be on a device")
+    device = _device_of(t.codes, "t.codes")
     dtype = t.dtype if dtype is None else dtype
-    dt = _float_type(dtype, tuple(_DTYPES), "dtype")
-    device = t.codes.get_device()
-    _check_tensor(t, "t", device)
+    dt = _float_type(dtype, _DTYPES, "dtype")
+    _check_tensor(t, "t", device, t.codes.dim() - 1)
     stream = stream_of(device)
     out = torch.empty(t.shape, dtype=dtype, device=t.codes.device)
     M = out.numel() // t.K
@@ -165,19 +172,19 @@ def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
     """codes uint8 [.., K/2] and scales uint8 [.., ceil(K/32)], as checkpoints hold
     them, on the device -> MXTensor (padded to whole slabs of 512 columns).  K:
     twice the codes' last dimension if None."""
-    if not isinstance(codes, torch.Tensor) or not codes.is_cuda or codes.dim() < 1:
-        raise ValueError("codes must be a device tensor of at least one dimension")
-    device = codes.get_device()
+    device = _device_of(codes, "codes")
+    if codes.dim() < 1:
+        raise ValueError("codes must have at least one dimension")
     check(codes, "codes", torch.uint8, codes.dim(), device)
     check(scales, "scales", torch.uint8, codes.dim(), device)
-    _float_type(dtype, tuple(_DTYPES), "dtype")
+    _float_type(dtype, _DTYPES, "dtype")
     K = 2 * codes.shape[-1] if K is None else K
     if K < 1 or K % 8:
         raise ValueError("K must be a positive multiple of 8")
     if (codes.shape[:-1] != scales.shape[:-1] or codes.shape[-1] != K // 2
             or scales.shape[-1] != -(-K // BLOCK)):
         raise ValueError("codes must be [.., K/2] and scales [.., ceil(K/32)]")
-    KG = _slabs(K)
+    KG = -(-K // 512)
     if codes.shape[-1] != 256 * KG:
         codes = torch.nn.functional.pad(codes, (0, 256 * KG - codes.shape[-1]))
     if scales.shape[-1] != 16 * KG:
@@ -197,10 +204,10 @@ def weight(t: MXTensor) -> MXWeight:
     """An MXTensor [N, K], or [E, N, K] for E experts, in the products' layout."""
     if not isinstance(t, MXTensor):
         raise TypeError("t must be an MXTensor")
+    device = _device_of(t.codes, "t.codes")
     if t.codes.dim() not in (3, 4):
         raise ValueError("t must be [N, K] or [E, N, K]")
-    device = t.codes.get_device()
-    _check_tensor(t, "t", device)
+    _check_tensor(t, "t", device, t.codes.dim() - 1)
     stream = stream_of(device)
     E, N = (1, *t.shape[:-1]) if t.codes.dim() == 3 else t.shape[:-1]
     qb, sb = weight_size(E, N, t.K)
@@ -218,34 +225,32 @@ def _check_weight(w: MXWeight, device: int) -> None:
     check(w.q, "w.q", torch.uint8, 1, device)
     check(w.s, "w.s", torch.uint8, 1, device)
     nt = w.E * -(-w.N // 16)
-    if w.q.numel() < nt * -(-w.K // 128) * 1024 or w.s.numel() < nt * _slabs(w.K) * 256:
+    if w.q.numel() < nt * -(-w.K // 128) * 1024 or w.s.numel() < nt * -(-w.K // 512) * 256:
         raise ValueError("MXWeight tensors are smaller than its shape needs")
 
 
 def _activations(x, K: int, dtype):
-    """(device, data, scales or None, x's dtype code, y's dtype code, y's dtype)"""
+    """(device, rows, pointer, pointer of the scales or None, x's dtype code, y's
+    dtype)"""
     if isinstance(x, MXTensor):
-        device = x.codes.get_device()
+        device = _device_of(x.codes, "x.codes")
         _check_tensor(x, "x", device, 2)
         if dtype is None:
             dtype = torch.bfloat16 if x.dtype == torch.float32 else x.dtype
-        data, scales, xt = x.codes, x.scales, 0
+        T, xK, data, scales, xt = x.codes.shape[1], x.K, x.codes.data_ptr(), x.scales.data_ptr(), 0
     else:
-        if not isinstance(x, torch.Tensor):
-            raise TypeError("x must be a torch.Tensor or an MXTensor")
-        xt = _float_type(x.dtype, (torch.float16, torch.bfloat16), "x")
-        device = x.get_device()
+        xt = _type_of(x, _DTYPES16, "x")
+        device = _device_of(x, "x")
         check(x, "x", x.dtype, 2, device)
-        if dtype not in (None, x.dtype):
+        if dtype is not None and dtype != x.dtype:
             raise TypeError("the results of 16-bit activations have their type")
-        dtype, data, scales = x.dtype, x, None
-    if device < 0:
-        raise ValueError("x must be on a device")
-    if x.shape[1] != K:
-        raise ValueError(f"x has K={x.shape[1]}, the weight K={K}")
-    return device, data, scales, xt, _float_type(dtype, (torch.float16, torch.bfloat16), "dtype"), dtype
+        dtype, (T, xK), data, scales = x.dtype, x.shape, x.data_ptr(), None
+    if xK != K:
+        raise ValueError(f"x has K={xK}, the weight K={K}")
+    return device, T, data, scales, xt, dtype
 
 
+@functools.lru_cache(maxsize=4096)
 def gemm_workspace_size(M: int, N: int, K: int, quantized: bool) -> int:
     b = ctypes.c_size_t()
     _raise(_mx().w4a16_mx_gemm_workspace_size(M, N, K, quantized, ctypes.byref(b)), "w4a16_mx_gemm_workspace_size")
@@ -264,28 +269,34 @@ def gemm(x, w: MXWeight, out: Optional[torch.Tensor] = None, dtype: Optional[tor
     workspace: at least gemm_workspace_size() bytes, for callers that manage
     their own; without one, a call that needs it takes a new block of torch's
     allocator (so calls on other streams, and captured ones, have their own)."""
-    device, data, scales, xt, yt, dtype = _activations(x, w.K, dtype)
+    if not isinstance(w, MXWeight):
+        raise TypeError("w must be an MXWeight")
+    device, M, data, scales, xt, dtype = _activations(x, w.K, dtype)
+    yt = _float_type(dtype, _DTYPES16, "dtype")
     _check_weight(w, device)
     if w.E != 1:
         raise ValueError("a weight of several experts goes to grouped_gemm")
-    M = x.shape[0]
     if out is None:
-        out = torch.empty((M, w.N), dtype=dtype, device=data.device)
+        out = torch.empty((M, w.N), dtype=dtype, device=w.q.device)
     else:
         check(out, "out", dtype, 2, device)
         if tuple(out.shape) != (M, w.N):
             raise ValueError("out must be [M, N]")
     stream = stream_of(device)
-    if M:
-        need = gemm_workspace_size(M, w.N, w.K, scales is not None)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=data.device) if need else None
-        elif workspace.get_device() != device or not workspace.is_contiguous():
+    if not M:
+        return out
+    ws, wsb = None, 0
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the call's device")
-        ws, wsb = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        _raise(_mx().w4a16_mx_gemm(data.data_ptr(), None if scales is None else scales.data_ptr(), xt, M, w.K,
-                                   w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(), ws, wsb, stream),
-               "w4a16_mx_gemm")
+        ws, wsb = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    else:
+        wsb = gemm_workspace_size(M, w.N, w.K, scales is not None)
+        if wsb:
+            workspace = w.q.new_empty(wsb)
+            ws = workspace.data_ptr()
+    _raise(_mx().w4a16_mx_gemm(data, scales, xt, M, w.K, w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(),
+                               ws, wsb, stream), "w4a16_mx_gemm")
     return out
 
 
@@ -298,27 +309,30 @@ def grouped_gemm(x, w: MXWeight, offsets: torch.Tensor, rows: Optional[torch.Ten
     less, rows int32 [R] (a row whose index lies outside 0..T-1 counts as
     zeros).  An expert may have no rows.  Rows of Y that no expert has stay as they
     are in `out`, and are undefined without one.  R may be 0."""
-    device, data, scales, xt, yt, dtype = _activations(x, w.K, dtype)
+    if not isinstance(w, MXWeight):
+        raise TypeError("w must be an MXWeight")
+    device, T, data, scales, xt, dtype = _activations(x, w.K, dtype)
+    yt = _float_type(dtype, _DTYPES16, "dtype")
     _check_weight(w, device)
     check(offsets, "offsets", torch.int32, 1, device)
     if offsets.shape[0] != w.E + 1:
         raise ValueError("offsets must be [E + 1]")
-    T = R = x.shape[0]
+    R = T
     if rows is not None:
         check(rows, "rows", torch.int32, 1, device)
         R = rows.shape[0]
     if out is None:
-        out = torch.empty((R, w.N), dtype=dtype, device=data.device)
+        out = torch.empty((R, w.N), dtype=dtype, device=w.q.device)
     else:
         check(out, "out", dtype, 2, device)
         if tuple(out.shape) != (R, w.N):
             raise ValueError("out must be [R, N]")
     stream = stream_of(device)
-    if R and not T:
+    if not R:
+        return out
+    if not T:
         raise ValueError("x has no rows")
-    if R:
-        _raise(_mx().w4a16_mx_grouped_gemm(
-            data.data_ptr(), None if scales is None else scales.data_ptr(), xt, T, w.K,
-            None if rows is None else rows.data_ptr(), R, offsets.data_ptr(), w.E, w.q.data_ptr(),
-            w.s.data_ptr(), w.N, yt, out.data_ptr(), stream), "w4a16_mx_grouped_gemm")
+    _raise(_mx().w4a16_mx_grouped_gemm(
+        data, scales, xt, T, w.K, None if rows is None else rows.data_ptr(), R, offsets.data_ptr(), w.E,
+        w.q.data_ptr(), w.s.data_ptr(), w.N, yt, out.data_ptr(), stream), "w4a16_mx_grouped_gemm")
     return out
