@@ -21,9 +21,7 @@
  *   codes   [2 KT][NT][2][16][16]: of 64 columns and 16 rows, the 16 bytes of
  *           each row's first block, then of its second;
  *   scales  [KG][16 NT][16]: of 512 columns the 16 scales of each row.
- * (What a tile of the products takes of 64 columns is one run of memory: with a
- * row's columns together, the tiles of a column block lie a power of two apart
- * for most K and share few of the L2's channels.)
+ * (What a tile of the products takes of 64 columns is one run of memory.)
  * Rows past N and columns past K hold zeros (scales: 127).
  */
 #ifndef W4A16_MX_H
@@ -115,6 +113,14 @@ int32_t w4a16_mx_check_grouped_gemm_args(const void *X, const uint8_t *x_scales,
                                          const int32_t *offsets, int64_t E, const void *q_dev,
                                          const void *s_dev, int64_t N, int32_t y_dtype,
                                          const void *Y);
+
+/* The kernel that a product of R rows runs (pure host): form[0] 0 the one for few
+ * rows, then form[1..3] its row tiles of 16, column tiles of 16 and waves along K;
+ * 1 the one for many, then form[1] its output tile (0 64 x 128, 1 64 x 256, 2
+ * 128 x 128, 3 128 x 256, 4 256 x 256) and form[2] the parts of K.  quantized:
+ * MXFP4 activations; grouped: w4a16_mx_grouped_gemm over E matrices (else E = 1). */
+int32_t w4a16_mx_kernel(int64_t R, int64_t E, int64_t N, int64_t K, int32_t quantized,
+                        int32_t grouped, int32_t *form);
 
 #ifdef __cplusplus
 }

@@ -145,3 +145,41 @@ def test_oracle_scales():
     x = torch.zeros((len(tops), 32))
     x[:, 7] = torch.tensor(tops)
     assert ref.quantize(x)[1][:, 0].tolist() == [0, 0, 0, 0, 1, 125, 125, 126, 127, 128, 252, 255, 255]
+
+
+# ---- the plans ------------------------------------------------------------------
+def test_kernel_args():
+    form = (ctypes.c_int32 * 4)()
+    f = mx._mx().w4a16_mx_kernel
+    assert f(4, 1, 40, 64, 0, 0, form) == w4.OK and f(4, 3, 40, 64, 1, 1, form) == w4.OK
+    assert f(4, 1, 40, 64, 0, 0, None) == w4.ERR_NULL
+    for bad in ((0, 1, 40, 64), (1 << 31, 1, 40, 64), (4, 2, 40, 64), (4, 1, 0, 64), (4, 1, 40, 60)):
+        assert f(*bad, 0, 0, form) == w4.ERR_SHAPE
+
+
+def form(R, N, K, quantized, experts=None):
+    """A form by what the kernels' instances differ in: with parts of K or without."""
+    k = mx.kernel(R, N, K, quantized, experts)
+    return k if k[0] == "small" else (k[0], k[1], k[2] > 1)
+
+
+def test_the_gpu_tests_have_a_shape_for_every_form():
+    """Every form that some call of wide ranges of sizes takes is among those of the
+    shapes that test_gpu_mx.py checks (and a split one has workspace)."""
+    import random
+
+    import test_gpu_mx as t
+    rng = random.Random(0)
+
+    def spread(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    have = {q: ({form(*s, q) for s in plain}, {form(*s[:3], q, s[3]) for s in grouped})
+            for q, plain, grouped in ((False, t.FORMS16, t.GROUPED16), (True, t.FORMS4, t.GROUPED4))}
+    for _ in range(6000):
+        q = rng.random() < 0.5
+        R, N, K = spread(1, 8192), spread(1, 32000), 8 * spread(1, 1400)
+        assert form(R, N, K, q) in have[q][0], (R, N, K, q)
+        assert (mx.gemm_workspace_size(R, N, K, q) > 0) == (mx.kernel(R, N, K, q)[2] > 1 and mx.kernel(R, N, K, q)[0] == "large")
+        R, N, K, E = spread(1, 30000), spread(1, 8000), 8 * spread(1, 800), spread(1, 256)
+        assert form(R, N, K, q, E) in have[q][1], (R, N, K, E, q)

@@ -64,18 +64,20 @@ int32_t check_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, i
 }  // namespace
 
 // The large kernel's output tiles: workgroups that share a compute unit, whether K
-// may be split over workgroups, and microseconds a stage (64 columns of 16-bit
-// activations, 256 of MXFP4): `alone`, what a workgroup needs at least (the copies'
-// latency), and `work`, what each adds to a busy compute unit.
+// may be split over workgroups, and microseconds: of a stage (64 columns of
+// 16-bit activations, 256 of MXFP4) what a workgroup needs at least (`alone`: the
+// copies' latency) and what each adds to a busy compute unit (`work`), and what a
+// tile takes besides (`tile`: its results' way out).  Fitted to 2048 x 22016 x
+// 4096, 61 .. 512 rows of the 7B model's projections, and 4096 tokens over 64 experts.
 struct MxTileCost {
     int shape, bm, bn, occ, split;
-    double alone, work;
+    double alone, work, tile;
 };
-const MxTileCost kTiles16[] = {{MX_64x128, 64, 128, 3, 1, 0.40, 0.235}, {MX_64x256, 64, 256, 2, 1, 0.52, 0.41},
-                               {MX_128x128, 128, 128, 2, 1, 0.55, 0.43}, {MX_128x256, 128, 256, 2, 1, 0.92, 0.82},
-                               {MX_256x256, 256, 256, 1, 0, 1.2, 1.62}};
-const MxTileCost kTiles4[] = {{MX_64x128, 64, 128, 2, 1, 0.62, 0.44}, {MX_128x128, 128, 128, 2, 1, 1.0, 0.63},
-                              {MX_128x256, 128, 256, 1, 0, 1.1, 1.1}, {MX_256x256, 256, 256, 1, 0, 1.8, 2.05}};
+const MxTileCost kTiles16[] = {{MX_64x128, 64, 128, 3, 1, 0.40, 0.25, 1.0}, {MX_64x256, 64, 256, 2, 1, 0.52, 0.44, 1.0},
+                               {MX_128x128, 128, 128, 2, 1, 0.55, 0.47, 0.5}, {MX_128x256, 128, 256, 2, 1, 0.92, 0.81, 1.0},
+                               {MX_256x256, 256, 256, 1, 0, 1.43, 1.43, 2.8}};
+const MxTileCost kTiles4[] = {{MX_64x128, 64, 128, 2, 1, 0.57, 0.30, 2.5}, {MX_128x128, 128, 128, 2, 1, 0.84, 0.45, 3.9},
+                              {MX_128x256, 128, 256, 1, 0, 0.98, 0.98, 6.7}, {MX_256x256, 256, 256, 1, 0, 1.87, 1.87, 5.0}};
 
 MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool grouped) {
     MxPlan p = {};
@@ -83,18 +85,27 @@ MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool groupe
     const double per = (double)R / (double)hit;   // and the rows of each
     const int64_t nt = (N + 15) / 16, kt = ktiles(K);
     p.splits = 1;
-    // Few rows: the memory-bound kernel.
-    p.large = grouped ? per > 8 : R > 32 || (R > 16 && nt * kt > (fp4 ? 32768 : 16384));
-    if (!p.large) {
-        p.mt = !grouped && R > 16 ? 2 : 1;
-        p.nb = grouped ? 4 : nt <= 384 ? 1 : nt <= 640 ? 2 : 3;
-        // waves along K until the chip has enough in all
-        const int64_t blocks = (nt + p.nb - 1) / p.nb * hit, enough = grouped ? 2300 : 1800;
-        p.ks = 1;
-        while (p.ks < 8 && blocks * p.ks < enough && p.ks * 2 <= kt)
-            p.ks *= 2;
-        return p;
+    // Few rows: the memory-bound kernel, as far as its traffic of activations (all
+    // rows once for every nb column tiles) stays beside that of the weights.  Both
+    // measured at 48 and 61 rows: 4096 x 4096 8.7 .. 10.2 us against 13.8 .. 14.5 in
+    // bf16, 22016 x 4096 24.1 .. 28.7 against 26.0 .. 26.3; quantized 6.3 .. 7.3 against
+    // 10.0 .. 11.8 and 17.2 .. 18.9 against 13.5.  A long K leaves more to the splits of
+    // the large kernel (61 x 4096 x 11008: 23.4 against 20.0).
+    if (grouped) {
+        // (8 experts of 4000 x 4096, 10 rows each in bf16: 22 us against 33)
+        p.large = per > (fp4 ? 6 : 8) && (fp4 || per > 24 || hit * nt > 4096);
+        p.mt = per > 8 ? 2 : 1;
+        p.nb = 4;
+        const int64_t blocks = (nt + 3) / 4 * hit;
+        p.ks = blocks < 1000 && p.mt == 1 ? 4 : blocks < 4096 ? 2 : 1;
+    } else {
+        p.large = R > 64 || (R > 32 && ((double)R * nt * kt > (fp4 ? 1.6e6 : 2.1e6) || (R > 48 && kt > 64)));
+        p.mt = (int)((R + 15) / 16);
+        p.nb = nt <= 256 ? 1 : nt <= 512 ? 2 : 3;
+        p.ks = p.mt <= 2 && ((p.mt == 2 && !fp4) || (p.nb == 1 && kt >= 64)) ? 8 : 4;
     }
+    if (!p.large)
+        return p;
     const int64_t stages = fp4 ? (K + 255) / 256 : (K + 63) / 64;
     const double most_bytes = 512.0 * (1 << 20);   // of splits' sums
     double best = 1e30;
@@ -111,9 +122,11 @@ MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool groupe
                 break;
             const double each = (double)((stages + sp - 1) / sp);
             const double rounds = (int64_t)((items * sp + 256 * t.occ - 1) / (256 * t.occ));
-            const double deep = (int64_t)((items * sp + 255) / 256);
-            const double alone = each * t.alone * rounds, work = each * t.work * deep;
-            double us = 1.5 * rounds + (alone > work ? alone : work);
+            const double fill = items * sp / 256;
+            // (workgroups that share a compute unit take up its idle ends)
+            const double deep = fill <= t.occ || t.occ == 1 ? (double)(int64_t)(fill + 0.999) : fill + 0.25;
+            const double alone = (each * t.alone + t.tile) * rounds, work = (each * t.work + t.tile) * deep;
+            double us = alone > work ? alone : work;
             if (sp > 1)
                 us += 2.0 + sum_bytes / 6e6;
             if (us < best) {
@@ -199,6 +212,21 @@ int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t qu
     if (st || M <= 0 || M >= (int64_t(1) << 31))
         return st ? st : W4A16_ERR_SHAPE;
     *bytes = plan_mx(M, 1, N, K, quantized != 0, false).ws_bytes;
+    return W4A16_OK;
+}
+
+int32_t w4a16_mx_kernel(int64_t R, int64_t E, int64_t N, int64_t K, int32_t quantized,
+                        int32_t grouped, int32_t *form) {
+    if (!form)
+        return W4A16_ERR_NULL;
+    const int32_t st = check_weight_shape(E, N, K);
+    if (st || R <= 0 || R >= (int64_t(1) << 31) || (!grouped && E != 1))
+        return st ? st : W4A16_ERR_SHAPE;
+    const MxPlan p = plan_mx(R, E, N, K, quantized != 0, grouped != 0);
+    form[0] = p.large;
+    form[1] = p.large ? p.shape : p.mt;
+    form[2] = p.large ? p.splits : p.nb;
+    form[3] = p.large ? 0 : p.ks;
     return W4A16_OK;
 }
 

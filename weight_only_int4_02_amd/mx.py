@@ -35,7 +35,7 @@ EXPORTS = ("w4a16_mx_quantize", "w4a16_mx_check_quantize_args", "w4a16_mx_dequan
            "w4a16_mx_check_dequantize_args", "w4a16_mx_weight_size", "w4a16_mx_weight",
            "w4a16_mx_check_weight_args", "w4a16_mx_gemm_workspace_size", "w4a16_mx_gemm",
            "w4a16_mx_check_gemm_args",
-           "w4a16_mx_grouped_gemm", "w4a16_mx_check_grouped_gemm_args")
+           "w4a16_mx_grouped_gemm", "w4a16_mx_check_grouped_gemm_args", "w4a16_mx_kernel")
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
 _DTYPES16 = {torch.float16: 0, torch.bfloat16: 1}
@@ -57,6 +57,7 @@ def _mx():
             getattr(L, f"w4a16_mx_{name}").argtypes = types + [P]
             getattr(L, f"w4a16_mx_check_{name}_args").argtypes = types
         L.w4a16_mx_gemm_workspace_size.argtypes = [I64, I64, I64, I32, PSZ]
+        L.w4a16_mx_kernel.argtypes = [I64, I64, I64, I64, I32, I32, ctypes.POINTER(I32)]
         L.w4a16_mx_weight_size.argtypes = [I64, I64, I64, PSZ, PSZ]
         for name in EXPORTS:
             getattr(L, name).restype = I32
@@ -248,6 +249,16 @@ def _activations(x, K: int, dtype):
     if xK != K:
         raise ValueError(f"x has K={xK}, the weight K={K}")
     return device, T, data, scales, xt, dtype
+
+
+def kernel(R: int, N: int, K: int, quantized: bool, experts: Optional[int] = None):
+    """The kernel that gemm() runs for R rows, or grouped_gemm() over `experts`
+    (pure host): ("small", row tiles, column tiles, waves along K) or ("large",
+    output tile, parts of K)."""
+    form = (ctypes.c_int32 * 4)()
+    _raise(_mx().w4a16_mx_kernel(R, experts or 1, N, K, quantized, experts is not None, form), "w4a16_mx_kernel")
+    tiles = ("64x128", "64x256", "128x128", "128x256", "256x256")
+    return ("large", tiles[form[1]], form[2]) if form[0] else ("small", *form[1:])
 
 
 @functools.lru_cache(maxsize=4096)
