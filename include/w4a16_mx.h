@@ -11,7 +11,7 @@
  * for 2^(b - 127), 255 for NaN.  A value is element times scale.
  *
  * Rows are held in whole slabs of 512 columns, KG = ceil(K / 512):
- *   codes   uint8 [2 KG][rows][128], of 256 columns the 128 bytes of a row, two
+ *   codes   uint8 [4 KG][rows][64], of 128 columns the 64 bytes of a row, two
  *           columns a byte, the first in the low half;
  *   scales  uint8 [KG][rows][16], the slab's 16 blocks of a row.
  * Columns from K on hold zeros (their scales: any but 255).  K is a multiple of

@@ -84,7 +84,7 @@ def test_quantize_odd_values(dt):
 
 def test_quantize_no_rows():
     t = mx.quantize(torch.empty((0, 64), device="cuda"))
-    assert t.codes.shape == (2, 0, 128) and t.scales.shape == (1, 0, 16)
+    assert t.codes.shape == (4, 0, 64) and t.scales.shape == (1, 0, 16)
     assert mx.dequantize(t).shape == (0, 64)
     assert mx.quantize(torch.empty((3, 0, 64), device="cuda", dtype=torch.float16)).shape == (3, 0, 64)
 
@@ -414,49 +414,67 @@ def test_captured_and_replayed(T):
 
 
 # ---- every form of the products -------------------------------------------------
-# (rows, N, K[, experts]): at least one shape for each form that the plans choose
+# (rows, N, K[, experts]): at least one shape for each form that the plans choose, and,
+# of those whose workgroups stay for tile after tile, K of one stage and of few
 FORMS16 = [(1, 1, 8), (3, 40, 9536), (2, 4536, 24), (7, 9880, 72), (20, 17, 136), (18, 4177, 40), (25, 8471, 8),
            (36, 33, 200), (41, 4146, 8), (33, 8909, 16), (60, 50, 328), (60, 6704, 8), (52, 13987, 8),
            (78, 31, 528), (65, 20, 72), (71, 20613, 2896), (322, 11038, 8), (3581, 3887, 280), (65, 18, 4440),
-           (86, 30, 304), (3204, 140, 1888), (131, 19918, 8)]
+           (86, 30, 304), (3204, 140, 1888), (131, 19918, 8), (6125, 3, 632), (4388, 883, 72), (16624, 62, 24),
+           (32253, 773, 152), (25549, 1105, 216), (30171, 289, 280)]
 FORMS4 = [(1, 1, 8), (3, 40, 8600), (2, 5635, 24), (7, 8644, 72), (18, 17, 136), (17, 40, 8376), (19, 4510, 8),
           (23, 9123, 8), (48, 33, 200), (36, 4389, 16), (35, 14559, 8), (63, 50, 328), (55, 7839, 8), (58, 13025, 8),
-          (5666, 2, 3336), (140, 11330, 8), (397, 12115, 272), (201, 18894, 8), (83, 30, 2200), (77, 20, 8)]
+          (5666, 2, 3336), (140, 11330, 8), (397, 12115, 272), (201, 18894, 8), (83, 30, 2200), (77, 20, 8),
+          (20865, 145, 392), (21869, 137, 688), (36870, 60, 56), (17035, 259, 280), (36775, 132, 736)]
 GROUPED16 = [(36, 30, 8, 1), (11311, 282, 8, 71), (3423, 3996, 592, 2), (46, 30, 264, 1), (2171, 431, 8, 211),
-             (80, 3599, 8, 146), (53, 1265, 8, 162), (5, 40, 72, 14), (9, 30, 16, 1)]
+             (80, 3599, 8, 146), (53, 1265, 8, 162), (5, 40, 72, 14), (9, 30, 16, 1), (9130, 1, 120, 251),
+             (10908, 67, 16, 199), (23426, 63, 40, 152), (27476, 61, 96, 146), (29784, 62, 152, 150)]
 GROUPED4 = [(11241, 30, 8, 189), (22443, 157, 320, 10), (15920, 151, 8, 76), (10, 30, 8, 1), (88, 3506, 8, 132),
-            (15, 4472, 8, 140), (3, 40, 72, 24)]
+            (15, 4472, 8, 140), (3, 40, 72, 24), (579, 262, 224, 88), (1155, 131, 344, 166), (1044, 192, 448, 153),
+            (858, 214, 616, 142), (967, 130, 56, 136), (26904, 65, 304, 153), (30205, 68, 632, 88)]
 
 
-def sampled(y, x, code, scale, quantized, rows_of, seed):
-    """Rows of a large product against the definition (all columns)."""
-    pick = torch.randperm(y.shape[0], generator=gen(seed))[:6]
-    for i in torch.cat([pick, torch.tensor([0, y.shape[0] - 1])]).tolist():
-        row, w = rows_of(i)
-        xv = ref.values(*ref.quantize(x[row:row + 1])) if quantized else x[row:row + 1].double()
-        wv = ref.values(code[w], scale[w])
-        wv = wv if quantized else wv.to(x.dtype).double()
-        compare(y[i:i + 1], *ref.product(xv, wv, y.dtype))
+def entering(x, quantized):
+    """(what the product is given, its values in 64 bits), on the device: the
+    quantization is tested above."""
+    if not quantized:
+        return x, x.double()
+    t = mx.quantize(x)
+    return t, mx.dequantize(t, torch.float32).double()
+
+
+def compare_all(y, X, W):
+    want, bound = ref.product(X, W, y.dtype)
+    off = (y.double() - want).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
+
+
+def weight_values(code, scale, dt, quantized):
+    W = ref.values(code, scale)
+    return (W if quantized else W.to(dt).double()).cuda()
 
 
 @pytest.mark.parametrize("quantized,shape", [(False, s) for s in FORMS16] + [(True, s) for s in FORMS4])
 def test_gemm_forms(shape, quantized):
     M, N, K = shape
-    x = torch.randn((M, K), generator=gen(M)).to(torch.bfloat16)
-    code, scale = random_weight((1, N, K), N)
-    y = mx.gemm(mx.quantize(x.cuda()) if quantized else x.cuda(), device_weight(code, scale))
-    sampled(y.cpu(), x, code, scale, quantized, lambda i: (i, 0), seed=K)
+    x = torch.randn((M, K), generator=gen(M)).to(torch.bfloat16).cuda()
+    code, scale = random_weight((N, K), N)
+    X, xv = entering(x, quantized)
+    compare_all(mx.gemm(X, device_weight(code, scale)), xv, weight_values(code, scale, x.dtype, quantized))
 
 
 @pytest.mark.parametrize("quantized,shape", [(False, s) for s in GROUPED16] + [(True, s) for s in GROUPED4])
 def test_grouped_forms(shape, quantized):
     R, N, K, E = shape
     T = R // 2 + 1
-    x = torch.randn((T, K), generator=gen(R)).half()
+    x = torch.randn((T, K), generator=gen(R)).half().cuda()
     code, scale = random_weight((E, N, K), N)
     ids = torch.randint(0, E, (R,), generator=gen(R + 1)).sort().values
     offsets = torch.searchsorted(ids, torch.arange(E + 1)).to(torch.int32)
-    rows = torch.randint(0, T, (R,), generator=gen(R + 2), dtype=torch.int32)
-    y = mx.grouped_gemm(mx.quantize(x.cuda()) if quantized else x.cuda(), device_weight(code, scale), offsets.cuda(),
-                        rows=rows.cuda())
-    sampled(y.cpu(), x, code, scale, quantized, lambda i: (int(rows[i]), int(ids[i])), seed=K)
+    rows = torch.randint(0, T, (R,), generator=gen(R + 2), dtype=torch.int32).cuda()
+    X, xv = entering(x, quantized)
+    y = mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(), rows=rows)
+    wv = weight_values(code, scale, x.dtype, quantized)
+    for e in range(E):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.stop > mine.start:
+            compare_all(y[mine], xv[rows[mine].long()], wv[e])

@@ -118,7 +118,7 @@ def test_grouped_args(kw, status):
 
 def test_the_binding_refuses_what_is_not_on_a_device():
     x = torch.zeros((2, 64), dtype=torch.float16)
-    t = mx.MXTensor(torch.zeros((2, 2, 128), dtype=torch.uint8), torch.zeros((1, 2, 16), dtype=torch.uint8), 64)
+    t = mx.MXTensor(torch.zeros((4, 2, 64), dtype=torch.uint8), torch.zeros((1, 2, 16), dtype=torch.uint8), 64)
     w = mx.MXWeight(torch.zeros(1024, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8), 1, 16, 64)
     for call in (lambda: mx.quantize(x), lambda: mx.dequantize(t), lambda: mx.gemm(x, w), lambda: mx.gemm(t, w),
                  lambda: mx.tensor(t.codes, t.codes),

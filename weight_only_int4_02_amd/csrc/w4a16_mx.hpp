@@ -13,7 +13,7 @@ enum MxX { MX_X_F16 = 0, MX_X_BF16 = 1, MX_X_FP4 = 2 };
 // One product: E matrices, rows sorted by matrix (a plain product has E = 1 and
 // no offsets).
 struct MxArgs {
-    const void *X;            // 16-bit [T][K], or codes [2 KG][T][128]
+    const void *X;            // 16-bit [T][K], or codes [4 KG][T][64]
     const uint8_t *xs;        // scales [KG][T][16] (codes only)
     const int32_t *rows;      // [R], or null: row i
     const int32_t *offsets;   // [E + 1], or null

@@ -74,8 +74,8 @@ struct MxTileCost {
     double alone, work, tile;
 };
 const MxTileCost kTiles16[] = {{MX_64x128, 64, 128, 3, 1, 0.40, 0.25, 1.0}, {MX_64x256, 64, 256, 2, 1, 0.52, 0.44, 1.0},
-                               {MX_128x128, 128, 128, 2, 1, 0.55, 0.47, 0.5}, {MX_128x256, 128, 256, 2, 1, 0.92, 0.81, 1.0},
-                               {MX_256x256, 256, 256, 1, 0, 1.43, 1.43, 2.8}};
+                               {MX_128x128, 128, 128, 2, 1, 0.55, 0.47, 1.5}, {MX_128x256, 128, 256, 2, 1, 0.92, 0.81, 1.0},
+                               {MX_256x256, 256, 256, 1, 0, 1.5, 1.5, 2.8}};
 const MxTileCost kTiles4[] = {{MX_64x128, 64, 128, 2, 1, 0.57, 0.30, 2.5}, {MX_128x128, 128, 128, 2, 1, 0.84, 0.45, 3.9},
                               {MX_128x256, 128, 256, 1, 0, 0.98, 0.98, 6.7}, {MX_256x256, 256, 256, 1, 0, 1.87, 1.87, 5.0}};
 
@@ -113,6 +113,8 @@ MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool groupe
     const int n = fp4 ? 4 : 5;
     for (int k = 0; k < n; k++) {
         const MxTileCost &t = tiles[k];
+        if (fp4 && grouped && t.shape == MX_128x256 && kt < 2)
+            continue;    // (its ring of four stages has scales of three slabs only)
         // (a matrix's last tile is half full on average)
         const double rows = grouped ? hit * (per <= t.bm / 2 ? 1.0 : per / t.bm + 0.5) : (double)((R + t.bm - 1) / t.bm);
         const double items = rows * (double)((N + t.bn - 1) / t.bn);
@@ -125,7 +127,9 @@ MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool groupe
             const double fill = items * sp / 256;
             // (workgroups that share a compute unit take up its idle ends)
             const double deep = fill <= t.occ || t.occ == 1 ? (double)(int64_t)(fill + 0.999) : fill + 0.25;
-            const double alone = (each * t.alone + t.tile) * rounds, work = (each * t.work + t.tile) * deep;
+            // (finding an expert's tile, where workgroups do not stay)
+            const double tile = !grouped ? t.tile : t.shape == MX_128x256 && fp4 ? 5.5 : t.split ? t.tile + 1.5 : t.tile;
+            const double alone = (each * t.alone + tile) * rounds, work = (each * t.work + tile) * deep;
             double us = alone > work ? alone : work;
             if (sp > 1)
                 us += 2.0 + sum_bytes / 6e6;

@@ -53,44 +53,53 @@ __device__ __forceinline__ void used_up() {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
-// Where block `b` of row `row` stands among the row's 8: any 8 or 16 consecutive
-// rows' blocks of one number lie in different banks.
+// Where block `b` of row `row` stands among the row's 4 (MXFP4) or 8: any 8 or 16
+// consecutive rows' blocks of one number lie in different banks.
+template <bool FP4>
 __device__ __forceinline__ uint32_t swizzle(uint32_t row, uint32_t b) {
-    return b ^ (row & 7) ^ ((row >> 3) & 1);
+    return FP4 ? b ^ ((row >> 1) & 3) ^ ((row >> 3) & 1) : b ^ (row & 7) ^ ((row >> 3) & 1);
 }
 
-// f with 0 .. 3, known when it is compiled.
-template <typename F>
-__device__ __forceinline__ void four(F f) {
+// f with 0 .. N - 1, known when it is compiled (N 2 or 4).
+template <int N, typename F>
+__device__ __forceinline__ void steps(F f) {
     f(std::integral_constant<int, 0>{});
     f(std::integral_constant<int, 1>{});
-    f(std::integral_constant<int, 2>{});
-    f(std::integral_constant<int, 3>{});
+    if constexpr (N == 4) {
+        f(std::integral_constant<int, 2>{});
+        f(std::integral_constant<int, 3>{});
+    }
 }
 
-template <int XT, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY, bool GROUPED>
+template <int XT, int KC, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY, bool GROUPED>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, OCC * (BM / WM) * (BN / WN) / 4)
 void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     constexpr bool FP4 = XT == MX_X_FP4;
     constexpr bool SPLIT = !STAY && !GROUPED;        // K may be split over workgroups
     constexpr int WAVES_N = BN / WN, WAVES = BM / WM * WAVES_N;
     constexpr int TM = WM / 32, TN = WN / 32;
-    constexpr int XROW = 128;                        // bytes of a stage's row
-    constexpr int SPS = FP4 ? 2 : 8;                 // stages of a slab
-    constexpr int XCH = BM / 8;                      // copies of 1 KiB of a stage: activations,
-    constexpr int WCH = FP4 ? BN / 8 : BN / 32;      // weights;
+    static_assert(FP4 ? KC == 128 || KC == 256 : KC == 64, "columns of a stage");
+    constexpr int KQ = KC / 64;                      // of 64 columns each
+    constexpr int H = FP4 ? KC / 128 : 1;            // parts of a stage's rows: 128 columns of
+    constexpr int XROW = FP4 ? 64 : 128;             // MXFP4 or 64 of 16 bits, in bytes
+    constexpr int RPC = 1024 / XROW, LPR = XROW / 16;    // rows of a copy, lanes of a row
+    constexpr int SPS = 512 / KC;                    // stages of a slab
+    constexpr int XPH = BM / RPC, XCH = H * XPH;     // copies of 1 KiB of a stage: activations,
+    constexpr int WCH = KQ * BN / 32;                // weights;
     constexpr int SX = FP4 ? BM / 64 : 0, SCH = BN / 64 + SX;   // of a slab: scales
     static_assert(XCH % WAVES == 0 && WCH % WAVES == 0, "copies split evenly over the waves");
     constexpr int KX = XCH / WAVES, KW = WCH / WAVES, KSC = (SCH + WAVES - 1) / WAVES;
     constexpr int CPW = KX + KW;                     // copies of a wave and stage
     static_assert((NBUF - 1) * (CPW + KSC) < 64, "counted by vmcnt");
     constexpr int STAGE = (XCH + WCH) * 1024, SLAB = KSC * WAVES * 1024;
-    // slabs that the stages of the ring can belong to (of one tile; of tiles of one stage)
-    constexpr int NSLAB = STAY ? NBUF : (NBUF - 2) / SPS + 2;
+    // slabs that the stages of the ring can belong to: of one tile; of tiles of one
+    // stage each; of tiles of two and more, a ring of four reaches three at most
+    constexpr int NSLAB = !STAY ? (NBUF - 2) / SPS + 2 : NBUF < 4 ? NBUF : 3;
     constexpr int OUT = 32 * (WN > 64 ? WN : 64) * 2;    // a wave's results on their way
-    static_assert(WAVES * OUT <= (STAY ? 1 : NBUF) * STAGE, "they pass through the ring's stages that are free");
+    // (through the ring's stages that are free, or a place of their own)
+    constexpr bool OWN = WAVES * OUT > (STAY ? 1 : NBUF) * STAGE;
     constexpr int TABLE = STAY && GROUPED ? kMaxMatrices * 4 : 0;
-    __shared__ __attribute__((aligned(1024))) char lds[NBUF * STAGE + NSLAB * SLAB + TABLE];
+    __shared__ __attribute__((aligned(1024))) char lds[NBUF * STAGE + NSLAB * SLAB + TABLE + (OWN ? WAVES * OUT : 0)];
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -144,15 +153,17 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     };
 
     const uint32_t wbytes = (uint32_t)a.NT * (uint32_t)a.KT * 1024u, sbytes = (uint32_t)a.NT * (uint32_t)a.KG * 256u;
-    const uint32_t xrow = FP4 ? 128u : (uint32_t)a.K * 2u;
+    const uint32_t xrow = FP4 ? 64u : (uint32_t)a.K * 2u;
     const i4_t dx = make_desc(a.X, (uint32_t)(a.T * (FP4 ? a.KG * 256 : a.K * 2)));
     const i4_t dxs = make_desc(a.xs, FP4 ? (uint32_t)(a.T * a.KG * 16) : 0u);
 
     // The rows of X that a lane copies in a tile, as the index has them: of 8 a copy,
     // and of 64 a copy of scales.  (They are looked at when the tile's copies begin:
     // until then they may be on their way.)
+    static_assert(XPH % WAVES == 0, "the same rows in every part");
+    constexpr int KR = XPH / WAVES;
     struct Rows {
-        uint32_t x[KX], s[KSC];
+        uint32_t x[KR], s[KSC];
     };
     auto source_row = [&](const MxTile &t, int i) __attribute__((always_inline)) {
         uint32_t row = (uint32_t)(t.row0 + i);
@@ -163,8 +174,8 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     auto source_rows = [&](const MxTile &t) __attribute__((always_inline)) {
         Rows r;
 #pragma unroll
-        for (int k = 0; k < KX; k++)
-            r.x[k] = source_row(t, (wave + k * WAVES) * 8 + lane / 8);
+        for (int k = 0; k < KR; k++)
+            r.x[k] = source_row(t, (wave + k * WAVES) * RPC + lane / LPR);
 #pragma unroll
         for (int k = 0; k < KSC; k++) {
             const int c = wave + k * WAVES - BN / 64;
@@ -175,17 +186,17 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     // A lane's block of an activation row is the same in all of a wave's copies
     // (they are 16 rows apart or a multiple, and the order of blocks goes by the
     // row's number below 16).
-    static_assert(WAVES % 2 == 0, "a lane's copies have one order of blocks");
-    const uint32_t xblock = swizzle((uint32_t)(wave * 8 + lane / 8), (uint32_t)(lane % 8));
+    static_assert(WAVES * RPC % 16 == 0, "a lane's copies have one order of blocks");
+    const uint32_t xblock = swizzle<FP4>((uint32_t)(wave * RPC + lane / LPR), (uint32_t)(lane % LPR));
     // the tile whose stages are being copied, and its copies' offsets
     i4_t dw, ds;
-    uint32_t xo[KX], so[KSC];
+    uint32_t xo[KR], so[KSC];
     int nt0;
     auto begin = [&](const Item &it, const Rows &rows) __attribute__((always_inline)) {
         dw = make_desc((const char *)a.qd + (int64_t)it.t.e * wbytes, wbytes);
         ds = make_desc((const char *)a.sd + (int64_t)it.t.e * sbytes, sbytes);
 #pragma unroll
-        for (int k = 0; k < KX; k++)
+        for (int k = 0; k < KR; k++)
             xo[k] = rows.x[k] < (uint32_t)a.T ? rows.x[k] * xrow + 16u * xblock : kOutOfRange;
         nt0 = it.nb * (BN / 16);
 #pragma unroll
@@ -204,7 +215,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     };
     const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)lds;
     // the stages of a split
-    const int all = FP4 ? (a.K + 255) / 256 : (a.K + 63) / 64;
+    const int all = (a.K + KC - 1) / KC;
     auto stage_from = [&](int split) __attribute__((always_inline)) {
         return SPLIT ? uniform(all * split / a.splits) : split * all;
     };
@@ -230,12 +241,12 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
 #pragma unroll
         for (int k = k0; k < (k1 < KX ? k1 : KX); k++)
             copy16(dx, to + (uint32_t)(wave + k * WAVES) * 1024u,
-                   none | (FP4 || (int)(8 * xblock) < a.K - s * 64 ? xo[k] : kOutOfRange),
-                   FP4 ? (uint32_t)s * (uint32_t)a.T * 128u : (uint32_t)(s * XROW));
+                   none | (FP4 || (int)(8 * xblock) < a.K - s * 64 ? xo[k % KR] : kOutOfRange),
+                   FP4 ? (uint32_t)(s * H + k / KR) * (uint32_t)a.T * 64u : (uint32_t)(s * XROW));
 #pragma unroll
         for (int k = (k0 > KX ? k0 - KX : 0); k < k1 - KX; k++) {
             const int c = wave + k * WAVES;
-            const int kq = FP4 ? 4 * s + c / (BN / 32) : s, two = nt0 + 2 * (c % (BN / 32));
+            const int kq = KQ * s + c / (BN / 32), two = nt0 + 2 * (c % (BN / 32));
             const int nt = two < a.NT ? two : a.NT - 1;
             const bool in = !none && (!FP4 || kq < 2 * a.KT);
             copy16(dw, to + (uint32_t)(XCH + c) * 1024u,
@@ -248,32 +259,43 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     // stage s; `between` is called in each of its four parts
     auto compute = [&](int s, int buf, int place, auto between) __attribute__((always_inline)) {
         const char *st = lds + buf * STAGE;
-        const char *x = st + (wm * WM + l32) * XROW;
+        const char *x = st + (wm * WM + l32) * XROW;      // (part 0)
         const char *w = st + XCH * 1024 + (wn * (WN / 16) + (l32 >> 4)) * 512 + h * 256 + (l32 & 15) * 16;
         const char *slab = lds + NBUF * STAGE + place * SLAB;
         const char *sw = slab + (wn * WN + l32) * 16, *sx = slab + (BN + wm * WM + l32) * 16;
         if constexpr (FP4) {
-            // of a row's two scale words of the stage, the lane's blocks in bytes 0 and 2
-            u2_t xs[TM], ws[TN];
+            // of a row's scale words of the stage, the lane's blocks in bytes 0 and 2
+            uint32_t xs[TM][H], ws[TN][H];
+            auto scales = [&](const char *from, uint32_t (&to)[H]) __attribute__((always_inline)) {
+                from += 4 * H * (s % SPS);
+                if constexpr (H == 2) {
+                    const u2_t v = *(const u2_t *)from >> (uint32_t)(8 * h);
+                    to[0] = v.x;
+                    to[1] = v.y;
+                } else {
+                    to[0] = *(const uint32_t *)from >> (8 * h);
+                }
+            };
 #pragma unroll
             for (int m = 0; m < TM; m++)
-                xs[m] = *(const u2_t *)(sx + 512 * m + 8 * (s & 1)) >> (uint32_t)(8 * h);
+                scales(sx + 512 * m, xs[m]);
 #pragma unroll
             for (int n = 0; n < TN; n++)
-                ws[n] = *(const u2_t *)(sw + 512 * n + 8 * (s & 1)) >> (uint32_t)(8 * h);
+                scales(sw + 512 * n, ws[n]);
             u4_t xa[2][TM], wa[2][TN];        // (the next 64 columns are read during these)
             auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
                 for (int m = 0; m < TM; m++)
-                    xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle((uint32_t)l32, (uint32_t)(2 * j + h)));
+                    xa[j & 1][m] = *(const u4_t *)(x + (j / 2 * BM + m * 32) * XROW +
+                                                   16 * swizzle<true>((uint32_t)l32, (uint32_t)(2 * (j & 1) + h)));
 #pragma unroll
                 for (int n = 0; n < TN; n++)
                     wa[j & 1][n] = *(const u4_t *)(w + n * 1024 + j * (BN * 32));
             };
             read(0);
-            four([&](auto jc) __attribute__((always_inline)) {     // 64 columns each
+            steps<KQ>([&](auto jc) __attribute__((always_inline)) {     // 64 columns each
                 constexpr int j = decltype(jc)::value;
-                if (j < 3)
+                if (j < KQ - 1)
                     read(j + 1);
 #pragma unroll
                 for (int n = 0; n < TN; n++) {
@@ -300,10 +322,10 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
             auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
                 for (int m = 0; m < TM; m++)
-                    xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle((uint32_t)l32, (uint32_t)(4 * h + j)));
+                    xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle<false>((uint32_t)l32, (uint32_t)(4 * h + j)));
             };
             read(0);
-            four([&](auto jc) __attribute__((always_inline)) {
+            steps<4>([&](auto jc) __attribute__((always_inline)) {
                 constexpr int j = decltype(jc)::value;
                 if (j < 3)
                     read(j + 1);
@@ -406,9 +428,9 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
                 // memory pipeline's queue and hold the waves up (2048 x 22016 x 4096 in
                 // bf16 293 -> 288 us)
                 compute(s, buf, place, [&](auto j) __attribute__((always_inline)) {
-                    constexpr int at = decltype(j)::value;
-                    issue(i.s, i.buf, none, std::integral_constant<int, CPW * at / 4>{},
-                          std::integral_constant<int, CPW * (at + 1) / 4>{});
+                    constexpr int at = decltype(j)::value, parts = FP4 ? KQ : 4;
+                    issue(i.s, i.buf, none, std::integral_constant<int, CPW * at / parts>{},
+                          std::integral_constant<int, CPW * (at + 1) / parts>{});
                 });
             }
             i.s += none ? 0 : 1;
@@ -420,7 +442,9 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
         used_up<!STAY>();
         const MxTile t = now.t;
         const int split = now.split, n0 = now.nb * BN + wn * WN;
-        char *out = lds + (STAY ? (buf == 0 ? NBUF - 1 : buf - 1) * STAGE : 0) + wave * OUT;
+        char *out = lds + wave * OUT + (OWN    ? NBUF * STAGE + NSLAB * SLAB + TABLE
+                                        : STAY ? (buf == 0 ? NBUF - 1 : buf - 1) * STAGE
+                                               : 0);
 #pragma unroll
         for (int m = 0; m < TM; m++) {
             const int i0 = wm * WM + 32 * m;
@@ -506,50 +530,58 @@ __global__ __launch_bounds__(kSumThreads) void mx_sum_kernel(MxArgs a, int64_t g
     }
 }
 
-template <int XT, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY>
+template <int XT, int KC, int BM, int BN, int WM, int WN, int NBUF, int OCC, bool STAY, bool GROUPED>
 int launch_inst(const MxArgs &a, bool ybf, hipStream_t st) {
     const int64_t blocks = (a.N + BN - 1) / BN;
+    // sum over the matrices with rows of ceil(rows / BM), at most
     const int64_t used = a.R < a.E ? a.R : a.E;
-    const int64_t tiles = a.offsets ? used + (a.R - used) / BM : (a.R + BM - 1) / BM;
+    const int64_t tiles = GROUPED ? used + (a.R - used) / BM : (a.R + BM - 1) / BM;
     const int64_t items = tiles * blocks * a.splits, most = STAY && items > kCus ? kCus : items;
     const int64_t grid = (most + kXcds - 1) / kXcds * kXcds;
     constexpr int threads = (BM / WM) * (BN / WN) * 64;
     if (items >= (int64_t(1) << 31) || grid * threads >= (int64_t(1) << 32))
         return (int)hipErrorInvalidConfiguration;
-    if (a.offsets) {
-        hipLaunchKernelGGL((mx_large_kernel<XT, BM, BN, WM, WN, NBUF, OCC, STAY, true>), dim3((unsigned)grid),
-                           dim3(threads), 0, st, a, (int)blocks, ybf);
-        return (int)hipGetLastError();
-    }
-    hipLaunchKernelGGL((mx_large_kernel<XT, BM, BN, WM, WN, NBUF, OCC, STAY, false>), dim3((unsigned)grid),
+    hipLaunchKernelGGL((mx_large_kernel<XT, KC, BM, BN, WM, WN, NBUF, OCC, STAY, GROUPED>), dim3((unsigned)grid),
                        dim3(threads), 0, st, a, (int)blocks, ybf);
     const int e = (int)hipGetLastError();
     if (e || a.splits == 1)
         return e;
     const int64_t groups = a.R * (a.NP / 4), wgs = (groups + kSumThreads - 1) / kSumThreads;
-    hipLaunchKernelGGL(mx_sum_kernel, dim3((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20)), dim3(kSumThreads), 0, st, a, groups,
-                       XT == MX_X_FP4 ? ybf : XT == MX_X_BF16);
+    hipLaunchKernelGGL(mx_sum_kernel, dim3((unsigned)(wgs < (1 << 20) ? wgs : 1 << 20)), dim3(kSumThreads), 0, st, a,
+                       groups, XT == MX_X_FP4 ? ybf : XT == MX_X_BF16);
     return (int)hipGetLastError();
 }
 
-template <int XT>
+template <int XT, bool GROUPED>
 int launch_shape(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
-    constexpr bool FP4 = XT == MX_X_FP4;
-    switch (p.shape) {
-    case MX_64x128: return launch_inst<XT, 64, 128, 32, 64, 3, FP4 ? 2 : 3, false>(a, ybf, st);
-    case MX_64x256:
-        if constexpr (!FP4)     // (plan_mx: never the cheapest)
-            return launch_inst<XT, 64, 256, 64, 64, 4, 2, false>(a, ybf, st);
-        break;
-    case MX_128x128: return launch_inst<XT, 128, 128, 64, 64, FP4 ? 2 : 3, 2, false>(a, ybf, st);
-    case MX_128x256:
-        if constexpr (FP4)
-            return launch_inst<XT, 128, 256, 64, 64, 2, 1, true>(a, ybf, st);
-        else
-            return launch_inst<XT, 128, 256, 128, 64, 3, 2, false>(a, ybf, st);
-    default: break;
+    if constexpr (XT == MX_X_FP4) {
+        switch (p.shape) {
+        case MX_64x128: return launch_inst<XT, 256, 64, 128, 32, 64, 3, 2, false, GROUPED>(a, ybf, st);
+        case MX_128x128: return launch_inst<XT, 256, 128, 128, 64, 64, 2, 2, false, GROUPED>(a, ybf, st);
+        case MX_128x256:
+            // (four stages of 128 columns where an expert's weights come from memory:
+            // 1000 tokens over 64 experts of 2816 x 2048 63 -> 56 us; two of 256 where they
+            // stay in the caches: 2048 x 22016 x 4096 128 -> 116)
+            if constexpr (GROUPED)
+                return launch_inst<XT, 128, 128, 256, 64, 64, 4, 1, true, GROUPED>(a, ybf, st);
+            else
+                return launch_inst<XT, 256, 128, 256, 64, 64, 2, 1, true, GROUPED>(a, ybf, st);
+        default: return launch_inst<XT, 256, 256, 256, 128, 64, 2, 1, true, GROUPED>(a, ybf, st);
+        }
+    } else {
+        switch (p.shape) {
+        case MX_64x128: return launch_inst<XT, 64, 64, 128, 32, 64, 3, 3, false, GROUPED>(a, ybf, st);
+        case MX_64x256: return launch_inst<XT, 64, 64, 256, 64, 64, 4, 2, false, GROUPED>(a, ybf, st);
+        case MX_128x128: return launch_inst<XT, 64, 128, 128, 64, 64, 3, 2, false, GROUPED>(a, ybf, st);
+        case MX_128x256: return launch_inst<XT, 64, 128, 256, 128, 64, 3, 2, false, GROUPED>(a, ybf, st);
+        default: return launch_inst<XT, 64, 256, 256, 128, 64, 3, 1, true, GROUPED>(a, ybf, st);
+        }
     }
-    return launch_inst<XT, 256, 256, 128, 64, FP4 ? 2 : 3, 1, true>(a, ybf, st);
+}
+
+template <int XT>
+int launch_any(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
+    return a.offsets ? launch_shape<XT, true>(a, p, ybf, st) : launch_shape<XT, false>(a, p, ybf, st);
 }
 
 }  // namespace
@@ -557,10 +589,10 @@ int launch_shape(const MxArgs &a, const MxPlan &p, bool ybf, hipStream_t st) {
 int launch_mx_large(const MxArgs &a, const MxPlan &p, int x, bool ybf, void *stream) {
     hipStream_t st = (hipStream_t)stream;
     if (x == MX_X_F16)
-        return launch_shape<MX_X_F16>(a, p, ybf, st);
+        return launch_any<MX_X_F16>(a, p, ybf, st);
     if (x == MX_X_BF16)
-        return launch_shape<MX_X_BF16>(a, p, ybf, st);
-    return launch_shape<MX_X_FP4>(a, p, ybf, st);
+        return launch_any<MX_X_BF16>(a, p, ybf, st);
+    return launch_any<MX_X_FP4>(a, p, ybf, st);
 }
 
 }  // namespace w4a16

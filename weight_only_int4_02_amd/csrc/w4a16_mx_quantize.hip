@@ -13,10 +13,7 @@ constexpr int kThreads = 256;
 // several places each.
 constexpr int64_t kMaxGroups = int64_t(1) << 23;
 
-unsigned groups(int64_t places) {
-    const int64_t n = (places + kThreads - 1) / kThreads;
-    return (unsigned)(n < kMaxGroups ? n : kMaxGroups);
-}
+unsigned groups(int64_t n) { return (unsigned)(n < kMaxGroups ? n : kMaxGroups); }
 
 // Eight values as fp32.  DT: 0 fp16, 1 bf16, 2 fp32.
 template <int DT>
@@ -48,20 +45,32 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
-// Sixteen lanes take a tile of 128 columns of one row, eight columns each; four
-// neighbours share a block.  The largest magnitude is found on the bits (whose
-// order is that of the magnitudes, NaN above infinity above numbers): its
-// exponent field less two is the scale byte.
+// A workgroup takes four rows of a slab of 512 columns: a wave 128 columns of
+// each, a lane eight of one row, so that reads are runs of 1 KiB (16 bits) and the
+// codes of a wave one run of 256 bytes (22016 x 4096 in bf16 47 us, 4.9 TB/s, its
+// inverse 34; with four tiles of one row a wave 88 together).  Four neighbouring
+// lanes share a block.  The largest magnitude is found on the bits (whose order is that of the magnitudes,
+// NaN above infinity above numbers): its exponent field less two is the scale byte.
+struct Place {
+    uint32_t row, kt;
+    bool in;
+};
+__device__ __forceinline__ Place place_of(uint32_t group, uint32_t M, uint32_t KG) {
+    const uint32_t rows = group / KG, slab = group - rows * KG, row = 4 * rows + ((threadIdx.x >> 4) & 3);
+    return {row, 4 * slab + (threadIdx.x >> 6), row < M};
+}
+
 template <int DT>
-__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *__restrict__ X,
-                                                               uint32_t tiles, uint32_t M, uint32_t KP,
-                                                               uint32_t K, uint32_t *__restrict__ codes,
+__global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *__restrict__ X, uint32_t M,
+                                                               uint32_t KG, uint32_t K, uint32_t n_groups,
+                                                               uint32_t *__restrict__ codes,
                                                                uint32_t *__restrict__ scales) {
     const uint32_t l = threadIdx.x & 15;
-    // (a group of 16 lanes leaves the loop as a whole)
-    for (uint32_t tile = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; tile < tiles;
-         tile += gridDim.x * (kThreads / 16)) {
-        const uint32_t row = tile / KP, kt = tile - row * KP, col = kt * 128 + 8 * l;
+    for (uint32_t group = blockIdx.x; group < n_groups; group += gridDim.x) {
+        const Place p = place_of(group, M, KG);
+        if (!p.in)                  // (whole groups of 16 lanes)
+            continue;
+        const uint32_t row = p.row, kt = p.kt, col = kt * 128 + 8 * l;
         float v[8] = {};
         if (col < K)
             load8<DT>(X, (int64_t)row * K + col, v);
@@ -83,7 +92,7 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *__res
         w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], s, 1);
         w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], s, 2);
         w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], s, 3);
-        codes[((int64_t)(kt >> 1) * M + row) * 32 + (kt & 1) * 16 + l] = byte == 255 ? 0 : w;
+        codes[((int64_t)kt * M + row) * 16 + l] = byte == 255 ? 0 : w;
         // the tile's four scale bytes in one word
         uint32_t b = byte << (8 * (l >> 2));
         b |= dpp<0x124>(b);            // rotated by 4 and by 8 lanes of 16
@@ -97,15 +106,15 @@ __global__ __launch_bounds__(kThreads) void mx_quantize_kernel(const void *__res
 template <int DT>
 __global__ __launch_bounds__(kThreads) void mx_dequantize_kernel(const uint32_t *__restrict__ codes,
                                                                  const uint32_t *__restrict__ scales,
-                                                                 uint32_t tiles, uint32_t M, uint32_t KP,
-                                                                 uint32_t K, void *__restrict__ Y) {
+                                                                 uint32_t M, uint32_t KG, uint32_t K,
+                                                                 uint32_t n_groups, void *__restrict__ Y) {
     const uint32_t l = threadIdx.x & 15;
-    for (uint32_t tile = blockIdx.x * (kThreads / 16) + threadIdx.x / 16; tile < tiles;
-         tile += gridDim.x * (kThreads / 16)) {
-        const uint32_t row = tile / KP, kt = tile - row * KP, col = kt * 128 + 8 * l;
-        if (col >= K)
+    for (uint32_t group = blockIdx.x; group < n_groups; group += gridDim.x) {
+        const Place p = place_of(group, M, KG);
+        const uint32_t row = p.row, kt = p.kt, col = kt * 128 + 8 * l;
+        if (!p.in || col >= K)
             continue;
-        const uint32_t w = codes[((int64_t)(kt >> 1) * M + row) * 32 + (kt & 1) * 16 + l];
+        const uint32_t w = codes[((int64_t)kt * M + row) * 16 + l];
         const float s = mx_scale(scales[((int64_t)(kt >> 2) * M + row) * 4 + (kt & 3)], l >> 2);
         const int64_t at = (int64_t)row * K + col;
         if constexpr (DT == 2) {
@@ -137,7 +146,7 @@ __global__ __launch_bounds__(kThreads) void mx_weight_kernel(const u4_t *__restr
         const int nt = (int)(piece - slab * NT), n = nt * 16 + r;
         const int64_t e = slab / (2 * KT), row = e * N + n;
         const int k = (int)(slab - e * 2 * KT), kt = k >> 1;
-        q[i] = n < N ? codes[((kt >> 1) * rows + row) * 8 + (kt & 1) * 4 + (k & 1) * 2 + b] : u4_t{0u, 0u, 0u, 0u};
+        q[i] = n < N ? codes[(kt * rows + row) * 4 + (k & 1) * 2 + b] : u4_t{0u, 0u, 0u, 0u};
         if (b == 0 && (k & 1) == 0) {
             uint32_t *to = s + (e * KG * NT * 16 + n) * 4;
             const int64_t step = (int64_t)NT * 64;
@@ -150,18 +159,19 @@ __global__ __launch_bounds__(kThreads) void mx_weight_kernel(const u4_t *__restr
 }
 
 template <int DT>
-int quantize_as(const void *X, uint32_t M, uint32_t KP, uint32_t K, uint8_t *codes, uint8_t *scales,
-                hipStream_t st) {
-    hipLaunchKernelGGL((mx_quantize_kernel<DT>), dim3(groups((int64_t)M * KP * 16)), dim3(kThreads), 0, st, X,
-                       M * KP, M, KP, K, (uint32_t *)codes, (uint32_t *)scales);
+int quantize_as(const void *X, uint32_t M, uint32_t K, uint8_t *codes, uint8_t *scales, hipStream_t st) {
+    const uint32_t KG = (K + 511) / 512, n = (M + 3) / 4 * KG;
+    hipLaunchKernelGGL((mx_quantize_kernel<DT>), dim3(groups(n)), dim3(kThreads), 0, st, X, M, KG, K, n,
+                       (uint32_t *)codes, (uint32_t *)scales);
     return (int)hipGetLastError();
 }
 
 template <int DT>
-int dequantize_as(const uint8_t *codes, const uint8_t *scales, uint32_t M, uint32_t KP, uint32_t K,
-                  void *Y, hipStream_t st) {
-    hipLaunchKernelGGL((mx_dequantize_kernel<DT>), dim3(groups((int64_t)M * KP * 16)), dim3(kThreads), 0, st,
-                       (const uint32_t *)codes, (const uint32_t *)scales, M * KP, M, KP, K, Y);
+int dequantize_as(const uint8_t *codes, const uint8_t *scales, uint32_t M, uint32_t K, void *Y,
+                  hipStream_t st) {
+    const uint32_t KG = (K + 511) / 512, n = (M + 3) / 4 * KG;
+    hipLaunchKernelGGL((mx_dequantize_kernel<DT>), dim3(groups(n)), dim3(kThreads), 0, st,
+                       (const uint32_t *)codes, (const uint32_t *)scales, M, KG, K, n, Y);
     return (int)hipGetLastError();
 }
 
@@ -169,27 +179,27 @@ int dequantize_as(const uint8_t *codes, const uint8_t *scales, uint32_t M, uint3
 
 int launch_mx_quantize(const void *X, int dtype, int64_t M, int64_t K, uint8_t *codes,
                        uint8_t *scales, void *stream) {
-    const uint32_t m = (uint32_t)M, k = (uint32_t)K, KP = (k + 511) / 512 * 4;
+    const uint32_t m = (uint32_t)M, k = (uint32_t)K;
     hipStream_t st = (hipStream_t)stream;
-    return dtype == 0   ? quantize_as<0>(X, m, KP, k, codes, scales, st)
-           : dtype == 1 ? quantize_as<1>(X, m, KP, k, codes, scales, st)
-                        : quantize_as<2>(X, m, KP, k, codes, scales, st);
+    return dtype == 0   ? quantize_as<0>(X, m, k, codes, scales, st)
+           : dtype == 1 ? quantize_as<1>(X, m, k, codes, scales, st)
+                        : quantize_as<2>(X, m, k, codes, scales, st);
 }
 
 int launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K,
                          int dtype, void *Y, void *stream) {
-    const uint32_t m = (uint32_t)M, k = (uint32_t)K, KP = (k + 511) / 512 * 4;
+    const uint32_t m = (uint32_t)M, k = (uint32_t)K;
     hipStream_t st = (hipStream_t)stream;
-    return dtype == 0   ? dequantize_as<0>(codes, scales, m, KP, k, Y, st)
-           : dtype == 1 ? dequantize_as<1>(codes, scales, m, KP, k, Y, st)
-                        : dequantize_as<2>(codes, scales, m, KP, k, Y, st);
+    return dtype == 0   ? dequantize_as<0>(codes, scales, m, k, Y, st)
+           : dtype == 1 ? dequantize_as<1>(codes, scales, m, k, Y, st)
+                        : dequantize_as<2>(codes, scales, m, k, Y, st);
 }
 
 int launch_mx_weight(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N, int64_t K,
                      void *q_dev, void *s_dev, void *stream) {
     const int KT = (int)((K + 127) / 128), NT = (int)((N + 15) / 16), KG = (KT + 3) / 4;
     const int64_t blocks = E * NT * KT * 64;
-    hipLaunchKernelGGL(mx_weight_kernel, dim3(groups(blocks)), dim3(kThreads), 0, (hipStream_t)stream,
+    hipLaunchKernelGGL(mx_weight_kernel, dim3(groups((blocks + kThreads - 1) / kThreads)), dim3(kThreads), 0, (hipStream_t)stream,
                        (const u4_t *)codes, (const uint32_t *)scales, blocks, E * N, (int)N, KT, NT, KG,
                        (u4_t *)q_dev, (uint32_t *)s_dev);
     return (int)hipGetLastError();

@@ -104,7 +104,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
 #pragma unroll
         for (int m = 0; m < MT; m++) {
             const uint32_t i = source_row(16 * m + row);
-            xo[m][c] = i != ~0u ? i * (FP4 ? 128u : (uint32_t)a.K * 2u) + 16u * b : kOutOfRange;
+            xo[m][c] = i != ~0u ? i * (FP4 ? 64u : (uint32_t)a.K * 2u) + 16u * b : kOutOfRange;
         }
     }
 #pragma unroll
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
             for (int c = 0; c < XC; c++)
                 copy16(dx, ring + (uint32_t)(d * SLOT + (m * XC + c) * 1024),
                        in && (FP4 || (int)xcol[c] < a.K - kt * 128) ? xo[m][c] : kOutOfRange,
-                       !in ? 0u : FP4 ? (uint32_t)(kt >> 1) * (uint32_t)a.T * 128u + 64u * (kt & 1) : 256u * kt);
+                       !in ? 0u : FP4 ? (uint32_t)kt * (uint32_t)a.T * 64u : 256u * kt);
             if constexpr (FP4)
                 st[d].xs[m] = load4_nops(dxs, in ? xso[m] : kOutOfRange,
                                              in ? (uint32_t)(kt >> 2) * (uint32_t)a.T * 16u + 4u * (kt & 3) : 0u);

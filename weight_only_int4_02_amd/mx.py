@@ -67,8 +67,8 @@ def _mx():
 
 @dataclass
 class MXTensor:
-    """MXFP4 rows, owned by torch tensors: codes uint8 [2 KG, .., 128] (of 256
-    columns the 128 bytes of each row, two columns a byte, the first in the low half)
+    """MXFP4 rows, owned by torch tensors: codes uint8 [4 KG, .., 64] (of 128
+    columns the 64 bytes of each row, two columns a byte, the first in the low half)
     and scales uint8 [KG, .., 16] (of 512 columns the 16 scales of each row:
     2^(b - 127), 255 for NaN), KG = ceil(K / 512); columns from K on hold zeros.  dtype: the type dequantize() gives where none is named,
     and products too (bf16 for fp32)."""
@@ -120,8 +120,8 @@ def _check_tensor(t: MXTensor, name: str, device: int, rank: int) -> None:
     check(codes, name, torch.uint8, rank + 1, device)
     check(scales, name, torch.uint8, rank + 1, device)
     c, s = codes.shape, scales.shape
-    if rank < 1 or c[0] != 2 * KG or s[0] != KG or c[-1] != 128 or s[-1] != 16 or c[1:-1] != s[1:-1]:
-        raise ValueError(f"{name}: codes must be [{2 * KG}, .., 128] and scales [{KG}, .., 16] for K = {t.K}, "
+    if rank < 1 or c[0] != 4 * KG or s[0] != KG or c[-1] != 64 or s[-1] != 16 or c[1:-1] != s[1:-1]:
+        raise ValueError(f"{name}: codes must be [{4 * KG}, .., 64] and scales [{KG}, .., 16] for K = {t.K}, "
                          f"got {tuple(c)} and {tuple(s)}")
 
 
@@ -141,7 +141,7 @@ def quantize(x: torch.Tensor) -> MXTensor:
         raise ValueError("K must be a positive multiple of 8")
     stream = stream_of(device)
     KG = -(-K // 512)
-    codes = torch.empty((2 * KG, *rows, 128), dtype=torch.uint8, device=x.device)
+    codes = torch.empty((4 * KG, *rows, 64), dtype=torch.uint8, device=x.device)
     scales = codes.new_empty((KG, *rows, 16))
     M = x.numel() // K
     if M:
@@ -190,7 +190,7 @@ def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
         codes = torch.nn.functional.pad(codes, (0, 256 * KG - codes.shape[-1]))
     if scales.shape[-1] != 16 * KG:
         scales = torch.nn.functional.pad(scales, (0, 16 * KG - scales.shape[-1]), value=127)
-    codes = codes.unflatten(-1, (2 * KG, 128)).movedim(-2, 0).contiguous()
+    codes = codes.unflatten(-1, (4 * KG, 64)).movedim(-2, 0).contiguous()
     scales = scales.unflatten(-1, (KG, 16)).movedim(-2, 0).contiguous()
     return MXTensor(codes, scales, K, dtype)
 
