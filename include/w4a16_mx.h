@@ -45,8 +45,8 @@ extern "C" {
  * kept.  A block that holds an infinity or a NaN is NaN throughout: scale 255,
  * codes 0.
  * Limits: M < 2^31, K <= 2^24, 4 M KG < 2^31.
- * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE, W4A16_ERR_ALIGN (16 bytes each),
- * W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where two of the buffers
+ * overlap), W4A16_ERR_ALIGN (16 bytes each), W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_mx_quantize(const void *X, int32_t dtype, int64_t M, int64_t K, uint8_t *codes,
                           uint8_t *scales, void *stream);
 int32_t w4a16_mx_check_quantize_args(const void *X, int32_t dtype, int64_t M, int64_t K,
@@ -60,8 +60,8 @@ int32_t w4a16_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t
 int32_t w4a16_mx_check_dequantize_args(const uint8_t *codes, const uint8_t *scales, int64_t M,
                                        int64_t K, int32_t dtype, const void *Y);
 
-/* E matrices [N][K] (codes and scales as above, of E N rows) -> the device layout, one matrix after the other; w4a16_mx_weight_size has
- * the bytes of all E.
+/* E matrices [N][K] (codes and scales as above, of E N rows) -> the device
+ * layout, one matrix after the other; w4a16_mx_weight_size has the bytes of all E.
  * Limits: 1 <= E <= 1024, N < 2^22, K <= 2^20, one matrix's codes below 2 GiB. */
 int32_t w4a16_mx_weight_size(int64_t E, int64_t N, int64_t K, size_t *q_bytes, size_t *s_bytes);
 int32_t w4a16_mx_weight(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
@@ -79,8 +79,9 @@ int32_t w4a16_mx_check_weight_args(const uint8_t *codes, const uint8_t *scales, 
  * that is 0; quantized: x_scales given): fp32 sums of parts of K.  Calls that may
  * run at the same time need separate ones.
  * Limits: those of w4a16_mx_weight, M < 2^31, X below 2 GiB.
- * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y overlaps X or its
- * scales), W4A16_ERR_ALIGN (16 bytes each), W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y, X with its scales and
+ * the workspace overlap), W4A16_ERR_ALIGN (16 bytes each), W4A16_ERR_WORKSPACE,
+ * W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantized,
                                      size_t *bytes);
 int32_t w4a16_mx_gemm(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t M,

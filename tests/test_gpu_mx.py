@@ -413,6 +413,86 @@ def test_captured_and_replayed(T):
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
 
 
+@pytest.mark.parametrize("quantized", [False, True])
+def test_parts_of_k_captured_in_two_graphs(quantized):
+    """Products that split K keep their sums in a workspace: of two graphs each has
+    its own, and one that the caller gives is used."""
+    M, N, K = 61, 80, 11008
+    code, scale = random_weight((N, K), 80)
+    w = device_weight(code, scale)
+    need = mx.gemm_workspace_size(M, N, K, quantized)
+    assert need > 0
+    own = torch.full((need + 64,), 77, dtype=torch.uint8, device="cuda")
+    xs = [torch.randn((M, K), generator=gen(81 + i)).to(torch.bfloat16).cuda() for i in range(3)]
+    ops = [mx.quantize(x) if quantized else x for x in xs]
+    want = [mx.gemm(x, w) for x in ops]
+    assert torch.equal(mx.gemm(ops[0], w, workspace=own[:need]), want[0])
+    assert bool((own[need:] == 77).all())
+    graphs, out = [], []
+    for i in range(3):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out.append(mx.gemm(ops[i], w, workspace=own if i == 2 else None))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+        assert torch.equal(mx.gemm(ops[1], w), want[1])
+        for o in out:
+            o.zero_()
+        torch.cuda.synchronize()
+
+
+# ---- past 32 bits -----------------------------------------------------------------
+def test_quantize_past_32_bits():
+    """More than 2^31 elements, codes and bytes of each: the last rows."""
+    K, M = 8192, 600_000
+    x = torch.zeros((M, K), dtype=torch.float16, device="cuda")
+    tail = torch.randn((5, K), generator=gen(90)).half()
+    x[-5:] = tail.cuda()
+    t = mx.quantize(x)
+    del x
+    code, scale = canonical(mx.MXTensor(t.codes[:, -5:].contiguous(), t.scales[:, -5:].contiguous(), K))
+    want_code, want_scale = ref.quantize(tail)
+    assert torch.equal(code, want_code) and torch.equal(scale, want_scale)
+    y = mx.dequantize(t)
+    assert torch.equal(y[-5:].cpu().double(), ref.values(want_code, want_scale).half().double())
+    assert not bool(y[:1000].any())
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("rows,R", [(1, 70_000), (300, 70_000), (3, 90)])
+def test_grouped_past_32_bits(rows, R, quantized):
+    """Experts of more than 4 GiB together, and (of 70000 rows) results of more than
+    4 GiB: the last expert's, behind rows that no expert has."""
+    E, N, K = 40, 32768, 8192
+    code, scale = random_weight((1, 512, K), 91)
+    one = mx.tensor(ref.pack(code).cuda(), scale.cuda(), K)
+    size, nt = mx.weight_size(E, N, K), 512 // 16
+    assert size[0] > 2 ** 32 and (R < 100 or R * N * 2 > 2 ** 32)
+    w = mx.MXWeight(*(torch.zeros(b, dtype=torch.uint8, device="cuda") for b in size), E, N, K)
+    # the last 512 columns of the last expert, in the device layout
+    part = mx.weight(one)
+    for whole, of in ((w.q, part.q), (w.s, part.s)):
+        steps = 2 * K // 128 if whole is w.q else K // 512
+        whole.view(E, steps, N // 16, -1)[-1, :, -nt:] = of.view(steps, nt, -1)
+    x = torch.randn((rows, K), generator=gen(92)).to(torch.bfloat16)
+    offsets = torch.full((E + 1,), R - rows, dtype=torch.int32)
+    offsets[-1] = R
+    index = torch.zeros(R, dtype=torch.int32)
+    index[R - rows:] = torch.arange(rows)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    X, xv, wv = operands(x, code, scale, quantized)
+    mx.grouped_gemm(X, w, offsets.cuda(), rows=index.cuda(), out=out)
+    compare(out[R - rows:, -512:], *ref.product(xv, wv[0], torch.bfloat16))
+    assert not bool(out[R - rows:, :-512].any())
+    assert bool((out[:80] == 7.0).all()) and bool((out[R - rows - 80:R - rows] == 7.0).all())
+
+
 # ---- every form of the products -------------------------------------------------
 # (rows, N, K[, experts]): at least one shape for each form that the plans choose, and,
 # of those whose workgroups stay for tile after tile, K of one stage and of few

@@ -116,6 +116,30 @@ def test_grouped_args(kw, status):
     assert grouped(**kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(codes=P(0x1100)), dict(scales=P(0x1000)), dict(dtype=2, M=64, codes=P(0x4000)),
+    dict(codes=P(1 << 31)), dict(scales=P((1 << 30) + 512))])
+def test_quantize_overlaps(kw):
+    assert quantize(X=P(0x1000), **kw) == w4.ERR_SHAPE
+
+
+def test_the_workspace_overlaps_nothing():
+    shape = dict(M=61, K=11008, N=64)
+    need = mx.gemm_workspace_size(61, 64, 11008, False)
+    assert need > 0
+    assert gemm(**shape) == w4.OK
+    assert gemm(**shape, wsb=need) == w4.OK
+    assert gemm(**shape, wsb=need - 1) == w4.ERR_WORKSPACE
+    assert gemm(**shape, ws=None) == w4.ERR_NULL
+    assert gemm(**shape, ws=P((1 << 37) + 8)) == w4.ERR_ALIGN
+    for ws in (P((1 << 32) + 61 * 64 * 2 - 16), P((1 << 32) - need + 16), P()):      # Y's end and start, X
+        assert gemm(**shape, ws=ws) == w4.ERR_SHAPE
+    quantized = dict(M=61, K=11008, N=64, xs=P(1 << 31))
+    assert mx.gemm_workspace_size(61, 64, 11008, True) > 0
+    assert gemm(**quantized) == w4.OK
+    assert gemm(**quantized, ws=P((1 << 31) + 256)) == w4.ERR_SHAPE
+
+
 def test_the_binding_refuses_what_is_not_on_a_device():
     x = torch.zeros((2, 64), dtype=torch.float16)
     t = mx.MXTensor(torch.zeros((4, 2, 64), dtype=torch.uint8), torch.zeros((1, 2, 16), dtype=torch.uint8), 64)

@@ -159,6 +159,10 @@ int32_t w4a16_mx_check_quantize_args(const void *X, int32_t dtype, int64_t M, in
         return W4A16_ERR_NULL;
     if (!aligned(X, 16) || !aligned(codes, 16) || !aligned(scales, 16))
         return W4A16_ERR_ALIGN;
+    const int64_t x_bytes = M * K * (dtype == W4A16_MX_F32 ? 4 : 2), slabs = M * kslabs(K);
+    if (overlap(X, x_bytes, codes, slabs * 256) || overlap(X, x_bytes, scales, slabs * 16) ||
+        overlap(codes, slabs * 256, scales, slabs * 16))
+        return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
 
@@ -205,7 +209,13 @@ int32_t w4a16_mx_check_gemm_args(const void *X, const uint8_t *x_scales, int32_t
         return W4A16_ERR_NULL;
     if (!aligned(workspace, 16))
         return W4A16_ERR_ALIGN;
-    return workspace_bytes < need ? W4A16_ERR_WORKSPACE : W4A16_OK;
+    if (workspace_bytes < need)
+        return W4A16_ERR_WORKSPACE;
+    const int64_t ws = (int64_t)need, x_bytes = x_scales ? M * kslabs(K) * 256 : M * K * 2;
+    if (overlap(workspace, ws, X, x_bytes) || overlap(workspace, ws, Y, M * N * 2) ||
+        (x_scales && overlap(workspace, ws, x_scales, M * kslabs(K) * 16)))
+        return W4A16_ERR_SHAPE;
+    return W4A16_OK;
 }
 
 int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantized,

@@ -1,13 +1,14 @@
 // Products with MXFP4 weights for many rows (compute-bound).
 //
 // A workgroup's waves form a BM x BN tile of Y, WM x WN of it each, from stages
-// of K in a ring in LDS: 128 bytes of a row of activations, that is 256 columns
-// of MXFP4 or 64 of a 16-bit type.  Every wave copies its share of a stage by
+// of KC columns of K in a ring in LDS: 256 or 128 of MXFP4, 64 of a 16-bit type
+// (128 or 64 bytes of a row of activations).  Every wave copies its share of a stage by
 // buffer-to-LDS DMA, NBUF - 1 stages ahead of the products; the copies are inline
 // assembly that the compiler does not count, so that it never waits for one by
 // itself.  A stage holds the activation rows (gathered, if an index is given: a
-// lane of a copy has its own address) and the weights' 16 x 64 tiles as they lie.  Scales are copied a slab of 512 columns at a time, 16 bytes a
-// row, when the slab's first stage is.
+// lane of a copy has its own address) and the weights' 16 x 64 tiles as they lie.
+// Scales are copied a slab of 512 columns at a time, 16 bytes a row, when the
+// slab's first stage is.
 //
 // Matrix instructions of 32 x 32, the weights first, so that a lane ends with
 // four neighbouring columns of one row.  A lane's operand is 16 bytes, one block of
@@ -17,10 +18,22 @@
 // K are the same eight for both operands.
 //
 // LDS: the weights' 16-byte blocks lie in the order in which lanes read them.  A
-// row of activations is 8 blocks of 16 bytes, stored at the block's number XOR a
-// function of the row, so that the lanes of a read (one block of consecutive
-// rows) reach all banks.  Results leave through LDS too, 32 rows of a wave at a
-// time, so that a store writes whole runs of a row.
+// row of activations is 4 (MXFP4) or 8 blocks of 16 bytes, stored at the block's
+// number XOR a function of the row, so that the lanes of a read (one block of
+// consecutive rows) reach all banks.  Results leave through LDS too, 32 rows of a
+// wave at a time, so that a store writes whole runs of a row.
+//
+// The largest tiles stay: as many workgroups as compute units, each taking tile
+// after tile of its XCD's run, whose stages are one stream, so that the copies of
+// the next tile run while results leave (2048 x 22016 x 4096 quantized 147 -> 114 us
+// with its quantization).
+//
+// Bound by the matrix cores where there are many rows: 2048 x 4096 x 11008 in bf16
+// 157 us, 1.18 PFLOP/s (a large library product on this card: 1.39), 2048 tokens over
+// two of eight experts of 22016 x 4096 608, 1.22; quantized 2048 x 22016 x 4096 103,
+// 3.6 (fp4 operands of random codes, from registers alone: 6.5 at the power limit),
+// 4096 tokens over six of 64 experts of 2816 x 2048 127, 2.2: their last tiles are
+// padding, and a tile has eight stages only.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -157,7 +170,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     const i4_t dx = make_desc(a.X, (uint32_t)(a.T * (FP4 ? a.KG * 256 : a.K * 2)));
     const i4_t dxs = make_desc(a.xs, FP4 ? (uint32_t)(a.T * a.KG * 16) : 0u);
 
-    // The rows of X that a lane copies in a tile, as the index has them: of 8 a copy,
+    // The rows of X that a lane copies in a tile, as the index has them: of RPC a copy,
     // and of 64 a copy of scales.  (They are looked at when the tile's copies begin:
     // until then they may be on their way.)
     static_assert(XPH % WAVES == 0, "the same rows in every part");
@@ -184,7 +197,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
         return r;
     };
     // A lane's block of an activation row is the same in all of a wave's copies
-    // (they are 16 rows apart or a multiple, and the order of blocks goes by the
+    // (which are 16 rows apart or a multiple, and the order of blocks goes by the
     // row's number below 16).
     static_assert(WAVES * RPC % 16 == 0, "a lane's copies have one order of blocks");
     const uint32_t xblock = swizzle<FP4>((uint32_t)(wave * RPC + lane / LPR), (uint32_t)(lane % LPR));

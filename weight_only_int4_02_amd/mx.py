@@ -70,8 +70,9 @@ class MXTensor:
     """MXFP4 rows, owned by torch tensors: codes uint8 [4 KG, .., 64] (of 128
     columns the 64 bytes of each row, two columns a byte, the first in the low half)
     and scales uint8 [KG, .., 16] (of 512 columns the 16 scales of each row:
-    2^(b - 127), 255 for NaN), KG = ceil(K / 512); columns from K on hold zeros.  dtype: the type dequantize() gives where none is named,
-    and products too (bf16 for fp32)."""
+    2^(b - 127), 255 for NaN), KG = ceil(K / 512); columns from K on hold zeros.
+    dtype: the type dequantize() gives where none is named, and products too (bf16
+    for fp32)."""
     codes: torch.Tensor
     scales: torch.Tensor
     K: int
@@ -120,7 +121,7 @@ def _check_tensor(t: MXTensor, name: str, device: int, rank: int) -> None:
     check(codes, name, torch.uint8, rank + 1, device)
     check(scales, name, torch.uint8, rank + 1, device)
     c, s = codes.shape, scales.shape
-    if rank < 1 or c[0] != 4 * KG or s[0] != KG or c[-1] != 64 or s[-1] != 16 or c[1:-1] != s[1:-1]:
+    if rank < 1 or KG < 1 or c[0] != 4 * KG or s[0] != KG or c[-1] != 64 or s[-1] != 16 or c[1:-1] != s[1:-1]:
         raise ValueError(f"{name}: codes must be [{4 * KG}, .., 64] and scales [{KG}, .., 16] for K = {t.K}, "
                          f"got {tuple(c)} and {tuple(s)}")
 
