@@ -138,7 +138,10 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     const uint32_t whole = tiles * (uint32_t)blocks_n, items = SPLIT ? whole * (uint32_t)a.splits : whole;
     const uint32_t first = items / kXcds * xcd + min(items % kXcds, xcd);
     const uint32_t run = items / kXcds + (items % kXcds > xcd ? 1 : 0);
-    const uint32_t mine = (uint32_t)uniform(run > wg ? (int)((run - wg + wgs - 1) / wgs) : 0);
+    // (round by round, each one on from the last: a matrix's last tiles have less work,
+    // and would fall to the same workgroups again and again)
+    const uint32_t rounds = run / wgs;
+    const uint32_t mine = (uint32_t)uniform((int)(rounds + ((wg + rounds) % wgs < run % wgs ? 1 : 0)));
     if (mine == 0)
         return;
     struct Item {
@@ -147,7 +150,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     };
     auto find = [&](uint32_t k) __attribute__((always_inline)) {
         Item it;
-        const uint32_t at = first + wg + k * wgs;
+        const uint32_t at = first + k * wgs + (wg + k) % wgs;
         it.split = SPLIT ? uniform((int)(at / whole)) : 0;
         const uint32_t item = at - (uint32_t)it.split * whole;
         if constexpr (GROUPED) {
@@ -269,16 +272,19 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     };
 
     f16_t acc[TM][TN];
-    // stage s; `between` is called in each of its four parts
-    auto compute = [&](int s, int buf, int place, auto between) __attribute__((always_inline)) {
+    // stage s of the wave's first MU row tiles; `between` is called in each of its parts
+    auto compute = [&](int s, int buf, int place, auto mu, auto between) __attribute__((always_inline)) {
+        constexpr int MU = decltype(mu)::value;
         const char *st = lds + buf * STAGE;
         const char *x = st + (wm * WM + l32) * XROW;      // (part 0)
         const char *w = st + XCH * 1024 + (wn * (WN / 16) + (l32 >> 4)) * 512 + h * 256 + (l32 & 15) * 16;
         const char *slab = lds + NBUF * STAGE + place * SLAB;
         const char *sw = slab + (wn * WN + l32) * 16, *sx = slab + (BN + wm * WM + l32) * 16;
-        if constexpr (FP4) {
+        if constexpr (MU == 0) {
+            steps<FP4 ? KQ : 4>(between);
+        } else if constexpr (FP4) {
             // of a row's scale words of the stage, the lane's blocks in bytes 0 and 2
-            uint32_t xs[TM][H], ws[TN][H];
+            uint32_t xs[MU][H], ws[TN][H];
             auto scales = [&](const char *from, uint32_t (&to)[H]) __attribute__((always_inline)) {
                 from += 4 * H * (s % SPS);
                 if constexpr (H == 2) {
@@ -290,15 +296,15 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
                 }
             };
 #pragma unroll
-            for (int m = 0; m < TM; m++)
+            for (int m = 0; m < MU; m++)
                 scales(sx + 512 * m, xs[m]);
 #pragma unroll
             for (int n = 0; n < TN; n++)
                 scales(sw + 512 * n, ws[n]);
-            u4_t xa[2][TM], wa[2][TN];        // (the next 64 columns are read during these)
+            u4_t xa[2][MU], wa[2][TN];        // (the next 64 columns are read during these)
             auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-                for (int m = 0; m < TM; m++)
+                for (int m = 0; m < MU; m++)
                     xa[j & 1][m] = *(const u4_t *)(x + (j / 2 * BM + m * 32) * XROW +
                                                    16 * swizzle<true>((uint32_t)l32, (uint32_t)(2 * (j & 1) + h)));
 #pragma unroll
@@ -313,7 +319,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
 #pragma unroll
                 for (int n = 0; n < TN; n++) {
 #pragma unroll
-                    for (int m = 0; m < TM; m++)
+                    for (int m = 0; m < MU; m++)
                         acc[m][n] = j % 2 == 0
                             ? mx_mfma32<0>(wa[j & 1][n], xa[j & 1][m], acc[m][n], ws[n][j / 2], xs[m][j / 2])
                             : mx_mfma32<2>(wa[j & 1][n], xa[j & 1][m], acc[m][n], ws[n][j / 2], xs[m][j / 2]);
@@ -331,10 +337,10 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
                 ws[n] = __builtin_bit_cast(float, (uint32_t)*(const uint8_t *)(sw + 512 * n + 2 * (s % SPS) + h) << 23);
                 wa[n] = *(const u4_t *)(w + n * 1024);
             }
-            u4_t xa[2][TM];
+            u4_t xa[2][MU];
             auto read = [&](int j) __attribute__((always_inline)) {
 #pragma unroll
-                for (int m = 0; m < TM; m++)
+                for (int m = 0; m < MU; m++)
                     xa[j & 1][m] = *(const u4_t *)(x + m * 32 * XROW + 16 * swizzle<false>((uint32_t)l32, (uint32_t)(4 * h + j)));
             };
             read(0);
@@ -346,7 +352,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
                 for (int n = 0; n < TN; n++) {
                     const u4_t v = mx_decode<XT == MX_X_BF16>(wa[n][j], ws[n]);
 #pragma unroll
-                    for (int m = 0; m < TM; m++) {
+                    for (int m = 0; m < MU; m++) {
                         if constexpr (XT == MX_X_BF16)
                             acc[m][n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                                 __builtin_bit_cast(bf8_t, v), __builtin_bit_cast(bf8_t, xa[j & 1][m]), acc[m][n], 0, 0, 0);
@@ -423,32 +429,49 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
 #pragma unroll
                 for (int e = 0; e < 16; e++)
                     acc[m][n][e] = 0.f;
-        for (int s = s0; s < s1; s++) {
-            // (copies of the NBUF - 2 stages after this one may be under way)
-            stage_ready<(NBUF - 2) * CPW>();
-            // (Behind the last stage of all, copies of nothing: zeros, read by nobody.)
-            const uint32_t none = next_stage() ? 0u : kOutOfRange;
-            if (s == s0)
-                look_ahead();
-            if (s == s0 || s % SPS == 0)
-                place = place + 1 < NSLAB ? place + 1 : 0;
-            if constexpr (NBUF == 2) {
-                // the copies have to land within this stage: all at once
-                issue(i.s, i.buf, none, std::integral_constant<int, 0>{}, std::integral_constant<int, CPW>{});
-                compute(s, buf, place, [](auto) {});
-            } else {
-                // a quarter at a time between the products: all at once they fill the
-                // memory pipeline's queue and hold the waves up (2048 x 22016 x 4096 in
-                // bf16 293 -> 288 us)
-                compute(s, buf, place, [&](auto j) __attribute__((always_inline)) {
-                    constexpr int at = decltype(j)::value, parts = FP4 ? KQ : 4;
-                    issue(i.s, i.buf, none, std::integral_constant<int, CPW * at / parts>{},
-                          std::integral_constant<int, CPW * (at + 1) / parts>{});
-                });
+        // Of a matrix's last tile a wave may have few rows or none, and leaves out their
+        // products: whole halves of its rows (4096 tokens over 64 experts of 2816 x
+        // 2048 quantized, with the order of tiles above, 136 -> 130 us; 1000 tokens
+        // 61 -> 59; 2048 over 8 of 22016 x 4096 282 -> 275).
+        auto stages = [&](auto mu) __attribute__((always_inline)) {
+            for (int s = s0; s < s1; s++) {
+                // (copies of the NBUF - 2 stages after this one may be under way)
+                stage_ready<(NBUF - 2) * CPW>();
+                // (Behind the last stage of all, copies of nothing: zeros, read by nobody.)
+                const uint32_t none = next_stage() ? 0u : kOutOfRange;
+                if (s == s0)
+                    look_ahead();
+                if (s == s0 || s % SPS == 0)
+                    place = place + 1 < NSLAB ? place + 1 : 0;
+                if constexpr (NBUF == 2) {
+                    // the copies have to land within this stage: all at once
+                    issue(i.s, i.buf, none, std::integral_constant<int, 0>{}, std::integral_constant<int, CPW>{});
+                    compute(s, buf, place, mu, [](auto) {});
+                } else {
+                    // a quarter at a time between the products: all at once they fill the
+                    // memory pipeline's queue and hold the waves up (2048 x 22016 x 4096 in
+                    // bf16 293 -> 288 us)
+                    compute(s, buf, place, mu, [&](auto j) __attribute__((always_inline)) {
+                        constexpr int at = decltype(j)::value, parts = FP4 ? KQ : 4;
+                        issue(i.s, i.buf, none, std::integral_constant<int, CPW * at / parts>{},
+                              std::integral_constant<int, CPW * (at + 1) / parts>{});
+                    });
+                }
+                i.s += none ? 0 : 1;
+                i.buf = i.buf + 1 < NBUF ? i.buf + 1 : 0;
+                buf = buf + 1 < NBUF ? buf + 1 : 0;
             }
-            i.s += none ? 0 : 1;
-            i.buf = i.buf + 1 < NBUF ? i.buf + 1 : 0;
-            buf = buf + 1 < NBUF ? buf + 1 : 0;
+        };
+        if constexpr (GROUPED) {
+            const int rows_of_wave = now.t.rows - wm * WM;
+            if (rows_of_wave <= 0)
+                stages(std::integral_constant<int, 0>{});
+            else if (TM > 1 && rows_of_wave <= WM / 2)
+                stages(std::integral_constant<int, (TM + 1) / 2>{});
+            else
+                stages(std::integral_constant<int, TM>{});
+        } else {
+            stages(std::integral_constant<int, TM>{});
         }
         // the results, 32 rows of the wave's at a time through its part of the stage
         // just used (the next copy there is issued after the next stage's barrier)
