@@ -25,14 +25,14 @@
 //
 // The largest tiles stay: as many workgroups as compute units, each taking tile
 // after tile of its XCD's run, whose stages are one stream, so that the copies of
-// the next tile run while results leave (2048 x 22016 x 4096 quantized 147 -> 114 us
-// with its quantization).
+// the next tile run while results leave (2048 x 22016 x 4096 in bf16 295 -> 281 us,
+// quantized 106 -> 104; 4096 tokens over 64 experts quantized 135 -> 128).
 //
 // Bound by the matrix cores where there are many rows: 2048 x 4096 x 11008 in bf16
 // 157 us, 1.18 PFLOP/s (a large library product on this card: 1.39), 2048 tokens over
-// two of eight experts of 22016 x 4096 608, 1.22; quantized 2048 x 22016 x 4096 103,
+// two of eight experts of 22016 x 4096 603, 1.23; quantized 2048 x 22016 x 4096 103,
 // 3.6 (fp4 operands of random codes, from registers alone: 6.5 at the power limit),
-// 4096 tokens over six of 64 experts of 2816 x 2048 127, 2.2: their last tiles are
+// 4096 tokens over six of 64 experts of 2816 x 2048 125, 2.3: their last tiles are
 // padding, and a tile has eight stages only.
 #include <hip/hip_runtime.h>
 
