@@ -558,3 +558,30 @@ def test_grouped_forms(shape, quantized):
         mine = slice(int(offsets[e]), int(offsets[e + 1]))
         if mine.stop > mine.start:
             compare_all(y[mine], xv[rows[mine].long()], wv[e])
+
+
+# rows of an expert around the halves of the rows of each wave, for all tiles
+LAST_ROWS = [1, 32, 33, 64, 65, 96, 97, 128, 129, 160, 161, 192, 193, 224, 225, 255, 256, 257, 320, 321, 384, 385,
+             448, 449, 0]
+
+
+@pytest.mark.parametrize("quantized,N,K,tile", [
+    (False, 16, 520, "64x128"), (False, 264, 520, "64x256"), (False, 520, 72, "128x128"), (False, 1000, 136, "128x256"),
+    (False, 6000, 136, "256x256"), (True, 16, 520, "64x128"), (True, 264, 72, "128x128"), (True, 1000, 520, "128x256"),
+    (True, 4100, 72, "256x256")])
+def test_grouped_last_tiles(quantized, N, K, tile):
+    E, R, T = len(LAST_ROWS), sum(LAST_ROWS), 500
+    assert mx.kernel(R, N, K, quantized, E)[:2] == ("large", tile)
+    x = torch.randn((T, K), generator=gen(N)).to(torch.bfloat16).cuda()
+    code, scale = random_weight((E, N, K), N + 1)
+    X, xv = entering(x, quantized)
+    w = device_weight(code, scale)
+    for order in (LAST_ROWS, LAST_ROWS[::-1]):
+        offsets = torch.tensor([0] + order).cumsum(0).to(torch.int32)
+        rows = torch.randint(0, T, (R,), generator=gen(N + 2), dtype=torch.int32).cuda()
+        y = mx.grouped_gemm(X, w, offsets.cuda(), rows=rows)
+        for e in range(E):
+            mine = slice(int(offsets[e]), int(offsets[e + 1]))
+            if mine.stop > mine.start:
+                compare_all(y[mine], xv[rows[mine].long()],
+                            weight_values(code[e], scale[e], x.dtype, quantized))
