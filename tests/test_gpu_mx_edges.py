@@ -1,0 +1,48 @@
+"""The microscaled 4-bit operators on the GPU at the ends of what their calls
+allow, against their definitions in 64 bits (oracle/mx.py)."""
+import pytest
+import torch
+
+from oracle import mx as ref
+from test_gpu_mx import compare, device_weight, gen, operands, random_weight
+from weight_only_int4_02_amd import mx
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+
+# ---- numbers of rows near 2^31 --------------------------------------------------
+@pytest.mark.parametrize("quantized", [False, True])
+def test_grouped_of_almost_2_to_the_31_rows(quantized):
+    """One expert has all rows but a few: its number of rows has no room for a tile
+    to be added in 32 bits."""
+    R, T, N, K = 2 ** 31 - 1, 5, 1, 8
+    x = torch.randn((T, K), generator=gen(1)).to(torch.bfloat16)
+    code, scale = random_weight((3, N, K), 2)
+    X, xv, wv = operands(x, code, scale, quantized)
+    rows = torch.randint(0, T, (R,), dtype=torch.int32, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    rows[1:T + 1] = torch.arange(T, dtype=torch.int32)
+    offsets = torch.tensor([0, 1, R - 3, R - 3], dtype=torch.int32)
+    out = torch.full((R, N), 77.0, dtype=torch.bfloat16, device="cuda")
+    mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(), rows=rows, out=out)
+    first = int(rows[0])
+    compare(out[:1], *ref.product(xv[first:first + 1], wv[0], torch.bfloat16))
+    compare(out[1:T + 1], *ref.product(xv, wv[1], torch.bfloat16))
+    assert bool((out[R - 3:] == 77.0).all())
+    each = out[1:T + 1, 0].clone()
+    for at in range(1, R - 3, 2 ** 28):
+        part = slice(at, min(at + 2 ** 28, R - 3))
+        assert torch.equal(out[part, 0], each[rows[part].long()])
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("R,N", [(1000, 40), (20000, 80), (20000, 520)])
+def test_grouped_offsets_that_fall_again_and_again(R, N, quantized):
+    """Half of the experts have all rows: nothing outside Y is written."""
+    E, K = 1024, 72
+    x = torch.randn((R, K), generator=gen(4)).half().cuda()
+    w = device_weight(*random_weight((E, N, K), 5))
+    offsets = torch.tensor([0, R] * (E // 2) + [0], dtype=torch.int32, device="cuda")
+    guard = torch.full((R + 128, N), 77.0, dtype=torch.float16, device="cuda")
+    mx.grouped_gemm(mx.quantize(x) if quantized else x, w, offsets, out=guard[64:R + 64])
+    assert bool((guard[:64] == 77.0).all()) and bool((guard[R + 64:] == 77.0).all())

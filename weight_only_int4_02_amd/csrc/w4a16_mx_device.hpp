@@ -120,27 +120,48 @@ __device__ __forceinline__ int mx_offset(const MxArgs &a, int e) {
 }
 
 // Sum over the wave's lanes up to the own one.
-__device__ __forceinline__ int wave_scan(int v, int lane) {
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, int lane) {
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
-        const int o = __shfl_up(v, d);
+        const uint32_t o = __shfl_up(v, d);
         v += lane >= d ? o : 0;
     }
     return v;
 }
 
+__device__ __forceinline__ uint32_t last_lane(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// Tiles of BM rows of matrix e, whose first row goes to `start` and rows to `total`.
+// (R may be 2^31 - 1: nothing is added to a number of rows.)
+template <int BM>
+__device__ __forceinline__ uint32_t mx_tiles_of(const MxArgs &a, int e, int &start, int &total) {
+    start = mx_offset(a, e);
+    total = mx_offset(a, e + 1) - start;
+    return total > 0 ? (uint32_t)(total - 1) / BM + 1 : 0;
+}
+
+// The tiles that all matrices have together at most.  Where offsets fall, their
+// ranges overlap and would have more: what is past these is left out, so that a sum
+// of tiles stays within 32 bits (64 matrices' 2^25 tiles of 64 rows each and these)
+// and the work within what the launch is for.
+template <int BM>
+__device__ __forceinline__ uint32_t mx_most_tiles(const MxArgs &a) {
+    const uint32_t R = (uint32_t)a.R, used = min(R, (uint32_t)a.E);
+    return used + (R - used) / BM;
+}
+
 // How many tiles of BM rows all matrices have together (by one wave).
 template <int BM>
-__device__ __forceinline__ int mx_count_tiles(const MxArgs &a, int lane) {
-    int total = 0;
+__device__ __forceinline__ uint32_t mx_count_tiles(const MxArgs &a, int lane) {
+    const uint32_t most = mx_most_tiles<BM>(a);
+    uint32_t total = 0;
     for (int base = 0; base < a.E; base += 64) {
         const int e = base + lane;
-        int n = 0;
-        if (e < a.E) {
-            const int r = mx_offset(a, e + 1) - mx_offset(a, e);
-            n = r > 0 ? (r + BM - 1) / BM : 0;
-        }
-        total += __builtin_amdgcn_readlane(wave_scan(n, lane), 63);
+        int start, rows;
+        const uint32_t n = e < a.E ? mx_tiles_of<BM>(a, e, start, rows) : 0;
+        total = min(total + last_lane(wave_scan(n, lane)), most);
     }
     return total;
 }
@@ -148,29 +169,26 @@ __device__ __forceinline__ int mx_count_tiles(const MxArgs &a, int lane) {
 // Tile `t` of all matrices' (by one wave; t is the same in all lanes); count 0
 // where there are not so many.
 template <int BM>
-__device__ __forceinline__ MxTile mx_find_tile(const MxArgs &a, int t, int lane) {
+__device__ __forceinline__ MxTile mx_find_tile(const MxArgs &a, uint32_t t, int lane) {
+    const uint32_t most = mx_most_tiles<BM>(a);
     MxTile out = {};
-    int before = 0;
+    uint32_t before = 0;
     for (int base = 0; base < a.E; base += 64) {
         const int e = base + lane;
-        int n = 0, o = 0, r = 0;
-        if (e < a.E) {
-            o = mx_offset(a, e);
-            r = mx_offset(a, e + 1) - o;
-            n = r > 0 ? (r + BM - 1) / BM : 0;
-        }
-        const int incl = before + wave_scan(n, lane);
+        int start = 0, total = 0;
+        const uint32_t n = e < a.E ? mx_tiles_of<BM>(a, e, start, total) : 0;
+        const uint32_t incl = min(before + wave_scan(n, lane), most);
         const uint64_t past = __ballot(incl > t);
         if (past) {
             const int l = __builtin_ctzll(past);
             out.e = base + l;
-            out.start = __builtin_amdgcn_readlane(o, l);
-            out.total = __builtin_amdgcn_readlane(r, l);
-            out.count = __builtin_amdgcn_readlane(n, l);
-            out.take(t - (__builtin_amdgcn_readlane(incl, l) - out.count), BM);
+            out.start = __builtin_amdgcn_readlane(start, l);
+            out.total = __builtin_amdgcn_readlane(total, l);
+            out.count = __builtin_amdgcn_readlane((int)n, l);
+            out.take((int)t - (__builtin_amdgcn_readlane((int)incl, l) - out.count), BM);
             return out;
         }
-        before = __builtin_amdgcn_readlane(incl, 63);
+        before = last_lane(incl);
     }
     return out;
 }
@@ -178,24 +196,22 @@ __device__ __forceinline__ MxTile mx_find_tile(const MxArgs &a, int t, int lane)
 // The same from a table in LDS of the tiles up to and with each matrix, made
 // once by one wave.
 template <int BM>
-__device__ __forceinline__ void mx_tile_table(const MxArgs &a, int *table, int lane) {
-    int before = 0;
+__device__ __forceinline__ void mx_tile_table(const MxArgs &a, uint32_t *table, int lane) {
+    const uint32_t most = mx_most_tiles<BM>(a);
+    uint32_t before = 0;
     for (int base = 0; base < a.E; base += 64) {
         const int e = base + lane;
-        int n = 0;
-        if (e < a.E) {
-            const int r = mx_offset(a, e + 1) - mx_offset(a, e);
-            n = r > 0 ? (r + BM - 1) / BM : 0;
-        }
-        const int incl = before + wave_scan(n, lane);
+        int start, total;
+        const uint32_t n = e < a.E ? mx_tiles_of<BM>(a, e, start, total) : 0;
+        const uint32_t incl = min(before + wave_scan(n, lane), most);
         if (e < a.E)
             table[e] = incl;
-        before = __builtin_amdgcn_readlane(incl, 63);
+        before = last_lane(incl);
     }
 }
 
 template <int BM>
-__device__ __forceinline__ MxTile mx_table_tile(const MxArgs &a, const int *table, int t, int lane) {
+__device__ __forceinline__ MxTile mx_table_tile(const MxArgs &a, const uint32_t *table, uint32_t t, int lane) {
     MxTile out = {};
     for (int base = 0; base < a.E; base += 64) {
         const int e = base + lane;
@@ -205,14 +221,14 @@ __device__ __forceinline__ MxTile mx_table_tile(const MxArgs &a, const int *tabl
             break;
         }
     }
-    const int before = __builtin_amdgcn_readfirstlane(out.e ? table[out.e - 1] : 0);
-    out.count = __builtin_amdgcn_readfirstlane(table[out.e]) - before;
+    const int before = __builtin_amdgcn_readfirstlane(out.e ? (int)table[out.e - 1] : 0);
+    out.count = __builtin_amdgcn_readfirstlane((int)table[out.e]) - before;
     // (scalar loads: a vector load would wait for the copies under way)
     const auto *offsets = (const __attribute__((address_space(4))) int *)(uintptr_t)a.offsets;
     const int R = (int)a.R, o = offsets[out.e], p = offsets[out.e + 1];
     out.start = o < 0 ? 0 : o > R ? R : o;
     out.total = (p < 0 ? 0 : p > R ? R : p) - out.start;
-    out.take(t - before, BM);
+    out.take((int)t - before, BM);
     return out;
 }
 

@@ -123,7 +123,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     // column block by column block of a matrix, its row tiles one after the other,
     // so that neighbours in time share the weights of a column block in their L2
     const uint32_t xcd = blockIdx.x % kXcds, wg = blockIdx.x / kXcds, wgs = gridDim.x / kXcds;
-    int *const table = (int *)(lds + NBUF * STAGE + NSLAB * SLAB);   // tiles up to each matrix
+    uint32_t *const table = (uint32_t *)(lds + NBUF * STAGE + NSLAB * SLAB);   // tiles up to each matrix
     uint32_t tiles;
     if constexpr (!GROUPED) {
         tiles = (uint32_t)((a.R + BM - 1) / BM);
@@ -131,9 +131,9 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
         if (wave == 0)
             mx_tile_table<BM>(a, table, lane);
         __syncthreads();
-        tiles = (uint32_t)__builtin_amdgcn_readfirstlane(table[a.E - 1]);
+        tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)table[a.E - 1]);
     } else {
-        tiles = (uint32_t)mx_count_tiles<BM>(a, lane);
+        tiles = mx_count_tiles<BM>(a, lane);
     }
     const uint32_t whole = tiles * (uint32_t)blocks_n, items = SPLIT ? whole * (uint32_t)a.splits : whole;
     const uint32_t first = items / kXcds * xcd + min(items % kXcds, xcd);
@@ -155,7 +155,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
         const uint32_t item = at - (uint32_t)it.split * whole;
         if constexpr (GROUPED) {
             const uint32_t any = (uint32_t)uniform((int)(item / (uint32_t)blocks_n));
-            it.t = STAY ? mx_table_tile<BM>(a, table, (int)any, lane) : mx_find_tile<BM>(a, (int)any, lane);
+            it.t = STAY ? mx_table_tile<BM>(a, table, any, lane) : mx_find_tile<BM>(a, any, lane);
             // (within the matrix: column block, then row tile)
             const uint32_t within = item - (any - (uint32_t)it.t.mt) * (uint32_t)blocks_n;
             it.nb = uniform((int)(within / (uint32_t)it.t.count));
@@ -182,7 +182,7 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
         uint32_t x[KR], s[KSC];
     };
     auto source_row = [&](const MxTile &t, int i) __attribute__((always_inline)) {
-        uint32_t row = (uint32_t)(t.row0 + i);
+        uint32_t row = (uint32_t)t.row0 + (uint32_t)i;
         if (GROUPED && a.rows)
             row = i < t.rows ? (uint32_t)a.rows[t.row0 + i] : ~0u;
         return i < t.rows ? row : ~0u;

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
     const int tile = blockIdx.x / blocks_n, block = blockIdx.x - tile * blocks_n;
     MxTile t;
     if constexpr (GROUPED) {
-        t = mx_find_tile<16 * MT>(a, tile, lane);
+        t = mx_find_tile<16 * MT>(a, (uint32_t)tile, lane);
         if (t.count == 0)
             return;
     } else {
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx_small_kernel(MxArgs a, int bloc
     // the last one: nothing), activations of each copy
     const uint32_t wo = (uint32_t)(kb >> 1) * (uint32_t)a.NT * 512u + 256u * (kb & 1) + 16u * r;
     auto source_row = [&](int i) __attribute__((always_inline)) {
-        uint32_t row = (uint32_t)(t.row0 + i);
+        uint32_t row = (uint32_t)t.row0 + (uint32_t)i;
         if (GROUPED && a.rows)
             row = i < t.rows ? (uint32_t)a.rows[t.row0 + i] : ~0u;
         return i < t.rows && row < (uint32_t)a.T ? row : ~0u;
