@@ -46,3 +46,22 @@ def test_grouped_offsets_that_fall_again_and_again(R, N, quantized):
     guard = torch.full((R + 128, N), 77.0, dtype=torch.float16, device="cuda")
     mx.grouped_gemm(mx.quantize(x) if quantized else x, w, offsets, out=guard[64:R + 64])
     assert bool((guard[:64] == 77.0).all()) and bool((guard[R + 64:] == 77.0).all())
+
+
+# ---- few rows of X, taken many times ---------------------------------------------
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("R,N", [(600, 40), (700, 264), (20000, 300)])
+@pytest.mark.parametrize("T,K", [(1, 8), (1, 72), (1, 200), (1, 512), (1, 1096), (3, 8), (7, 8), (2, 1032)])
+def test_grouped_one_row_for_many(T, K, R, N, quantized):
+    """X is shorter than the stages of the many rows' tiles."""
+    x = torch.randn((T, K), generator=gen(T + K)).to(torch.bfloat16)
+    code, scale = random_weight((2, N, K), K)
+    X, xv, wv = operands(x, code, scale, quantized)
+    rows = torch.randint(0, T, (R,), generator=gen(R), dtype=torch.int32)
+    offsets = torch.tensor([0, R // 3, R], dtype=torch.int32)
+    y = mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(), rows=rows.cuda())
+    for e in range(2):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        want, bound = ref.product(xv, wv[e], torch.bfloat16)
+        index = rows[mine].long()
+        compare(y[mine], want[index], bound[index])

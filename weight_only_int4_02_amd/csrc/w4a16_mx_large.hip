@@ -250,15 +250,18 @@ void mx_large_kernel(MxArgs a, int blocks_n, bool ybf) {
     };
     // and copies k0 .. k1 - 1 of the wave's CPW: activations, then weights, two tiles'
     // 64 columns a copy, 1 KiB as they lie.  (Past the last tile of rows the last one
-    // again, whose results nobody stores; past the last of K zeros.)
+    // again, whose results nobody stores; past the last of K, and where `none` is not
+    // 0, zeros: of vector offsets past the descriptor, beside scalar offsets that are
+    // within it, so that they do not rest on how the range check takes the two together.)
     auto issue = [&](int s, int buf, uint32_t none, auto k0_c, auto k1_c) __attribute__((always_inline)) {
         constexpr int k0 = decltype(k0_c)::value, k1 = decltype(k1_c)::value;
         const uint32_t to = lds0 + (uint32_t)(buf * STAGE);
+        const int sx = none ? 0 : s;
 #pragma unroll
         for (int k = k0; k < (k1 < KX ? k1 : KX); k++)
             copy16(dx, to + (uint32_t)(wave + k * WAVES) * 1024u,
                    none | (FP4 || (int)(8 * xblock) < a.K - s * 64 ? xo[k % KR] : kOutOfRange),
-                   FP4 ? (uint32_t)(s * H + k / KR) * (uint32_t)a.T * 64u : (uint32_t)(s * XROW));
+                   FP4 ? (uint32_t)(sx * H + k / KR) * (uint32_t)a.T * 64u : (uint32_t)(sx * XROW));
 #pragma unroll
         for (int k = (k0 > KX ? k0 - KX : 0); k < k1 - KX; k++) {
             const int c = wave + k * WAVES;
