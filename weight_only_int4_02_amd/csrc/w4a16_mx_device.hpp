@@ -19,15 +19,14 @@ typedef float f16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u2_t __attribute__((ext_vector_type(2)));
 
 // Copies 16 bytes a lane to LDS at lds + 16 lane; lds is the same in all lanes.
-// Out of range: zeros.  (M0, which the compiler uses for nothing else in these
-// kernels, holds the address.  Its write and the s_nop are the five wait states
-// that the load needs after a vector instruction wrote a scalar register it reads,
-// a spilled one's reload among them.  It names no memory: what it writes is read
-// behind the barrier of a later stage only, and reads of the present stage may be
-// moved past it.)
+// Out of range: zeros.  (M0 holds the address.  Its write and the s_nop are the five
+// wait states that the load needs after a vector instruction wrote a scalar
+// register it reads, a spilled one's reload among them.  The block names no memory:
+// what it writes is read behind the barrier of a later stage only, and reads of the
+// present stage may be moved past it.)
 __device__ __forceinline__ void copy16(i4_t desc, uint32_t lds, uint32_t voffset, uint32_t soffset) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-                 :: "s"(lds), "v"(voffset), "s"(desc), "s"(soffset));
+                 :: "s"(lds), "v"(voffset), "s"(desc), "s"(soffset) : "m0");
 }
 
 // Byte `b` of a register of four scales as the scale operand of a conversion.
