@@ -79,9 +79,9 @@ int32_t w4a16_mx_check_weight_args(const uint8_t *codes, const uint8_t *scales, 
  * that is 0; quantized: x_scales given): fp32 sums of parts of K.  Calls that may
  * run at the same time need separate ones.
  * Limits: those of w4a16_mx_weight, M < 2^31, X below 2 GiB.
- * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y, X with its scales and
- * the workspace overlap), W4A16_ERR_ALIGN (16 bytes each), W4A16_ERR_WORKSPACE,
- * W4A16_ERR_ARCH, W4A16_ERR_HIP. */
+ * Errors: W4A16_ERR_NULL, W4A16_ERR_SHAPE (also where Y or the workspace
+ * overlaps the other, X with its scales or the weight), W4A16_ERR_ALIGN (16 bytes
+ * each), W4A16_ERR_WORKSPACE, W4A16_ERR_ARCH, W4A16_ERR_HIP. */
 int32_t w4a16_mx_gemm_workspace_size(int64_t M, int64_t N, int64_t K, int32_t quantized,
                                      size_t *bytes);
 int32_t w4a16_mx_gemm(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t M,

@@ -4,7 +4,11 @@ import glob
 import os
 import re
 
-from weight_only_int4_02_amd import build
+import pytest
+
+import weight_only_int4_02_amd as w4
+from test_mx_abi import P, gemm, grouped
+from weight_only_int4_02_amd import build, mx
 
 
 def test_inline_assembly_that_writes_m0_says_so():
@@ -17,3 +21,31 @@ def test_inline_assembly_that_writes_m0_says_so():
     assert writes
     for block in writes:
         assert re.search(r':\s*"m0"', block), block
+
+
+# ---- results over weights --------------------------------------------------------
+@pytest.mark.parametrize("quantized", [False, True])
+def test_results_overlap_no_weight(quantized):
+    E, N, K = 3, 40, 264
+    xs = dict(xs=P(1 << 31)) if quantized else {}
+    for call, n in ((lambda **kw: gemm(N=N, K=K, **xs, **kw), 1), (lambda **kw: grouped(N=N, K=K, E=E, **xs, **kw), E)):
+        assert call() == w4.OK
+        q, s = mx.weight_size(n, N, K)
+        y = 4 * N * 2
+        for size, at in ((q, 1 << 33), (s, 1 << 34)):
+            for inside in (0, size - 16, 16 - y):
+                assert call(Y=P(at + inside)) == w4.ERR_SHAPE
+            for beside in (size, -y):
+                assert call(Y=P(at + beside)) == w4.OK
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_the_workspace_overlaps_no_weight(quantized):
+    shape = dict(M=61, N=64, K=11008, **(dict(xs=P(1 << 31)) if quantized else {}))
+    need = mx.gemm_workspace_size(61, 64, 11008, quantized)
+    assert need > 0 and need % 16 == 0 and gemm(**shape) == w4.OK
+    for size, at in zip(mx.weight_size(1, 64, 11008), (1 << 33, 1 << 34)):
+        for inside in (0, size - 16, 16 - need):
+            assert gemm(**shape, ws=P(at + inside)) == w4.ERR_SHAPE
+        for beside in (size, -need):
+            assert gemm(**shape, ws=P(at + beside)) == w4.OK

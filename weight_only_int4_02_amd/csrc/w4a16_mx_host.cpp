@@ -36,6 +36,14 @@ int32_t check_weight_shape(int64_t E, int64_t N, int64_t K) {
     return W4A16_OK;
 }
 
+int64_t weight_q_bytes(int64_t E, int64_t N, int64_t K) { return E * ((N + 15) / 16) * ktiles(K) * 1024; }
+int64_t weight_s_bytes(int64_t E, int64_t N, int64_t K) { return E * ((N + 15) / 16) * kslabs(K) * 256; }
+
+bool overlaps_weight(const void *p, int64_t bytes, const void *q_dev, const void *s_dev, int64_t E, int64_t N,
+                     int64_t K) {
+    return overlap(p, bytes, q_dev, weight_q_bytes(E, N, K)) || overlap(p, bytes, s_dev, weight_s_bytes(E, N, K));
+}
+
 // The rules that a product has with and without experts.
 int32_t check_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, int64_t T,
                       int64_t K, int64_t R, int64_t E, const void *q_dev, const void *s_dev,
@@ -56,7 +64,8 @@ int32_t check_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, i
         !aligned(x_scales, 16))
         return W4A16_ERR_ALIGN;
     if (overlap(X, x_bytes, Y, R * N * 2) ||
-        (x_scales && overlap(x_scales, T * kslabs(K) * 16, Y, R * N * 2)))
+        (x_scales && overlap(x_scales, T * kslabs(K) * 16, Y, R * N * 2)) ||
+        overlaps_weight(Y, R * N * 2, q_dev, s_dev, E, N, K))
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
@@ -177,9 +186,8 @@ int32_t w4a16_mx_weight_size(int64_t E, int64_t N, int64_t K, size_t *q_bytes, s
     const int32_t st = check_weight_shape(E, N, K);
     if (st)
         return st;
-    const int64_t nt = (N + 15) / 16, kt = ktiles(K);
-    *q_bytes = (size_t)(E * nt * kt * 1024);
-    *s_bytes = (size_t)(E * nt * kslabs(K) * 256);
+    *q_bytes = (size_t)weight_q_bytes(E, N, K);
+    *s_bytes = (size_t)weight_s_bytes(E, N, K);
     return W4A16_OK;
 }
 
@@ -213,7 +221,8 @@ int32_t w4a16_mx_check_gemm_args(const void *X, const uint8_t *x_scales, int32_t
         return W4A16_ERR_WORKSPACE;
     const int64_t ws = (int64_t)need, x_bytes = x_scales ? M * kslabs(K) * 256 : M * K * 2;
     if (overlap(workspace, ws, X, x_bytes) || overlap(workspace, ws, Y, M * N * 2) ||
-        (x_scales && overlap(workspace, ws, x_scales, M * kslabs(K) * 16)))
+        (x_scales && overlap(workspace, ws, x_scales, M * kslabs(K) * 16)) ||
+        overlaps_weight(workspace, ws, q_dev, s_dev, 1, N, K))
         return W4A16_ERR_SHAPE;
     return W4A16_OK;
 }
