@@ -62,7 +62,9 @@ int32_t w4a16_mx_check_dequantize_args(const uint8_t *codes, const uint8_t *scal
 
 /* E matrices [N][K] (codes and scales as above, of E N rows) -> the device
  * layout, one matrix after the other; w4a16_mx_weight_size has the bytes of all E.
- * Limits: 1 <= E <= 1024, N < 2^22, K <= 2^20, one matrix's codes below 2 GiB. */
+ * Limits: 1 <= E <= 1024, N < 2^22, K <= 2^20, one matrix's codes below 2 GiB.
+ * A result that overlaps the other or an input is refused too (W4A16_ERR_SHAPE),
+ * by w4a16_mx_weight itself: w4a16_mx_check_weight_args does not look at that. */
 int32_t w4a16_mx_weight_size(int64_t E, int64_t N, int64_t K, size_t *q_bytes, size_t *s_bytes);
 int32_t w4a16_mx_weight(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
                         int64_t K, void *q_dev, void *s_dev, void *stream);

@@ -49,3 +49,23 @@ def test_the_workspace_overlaps_no_weight(quantized):
             assert gemm(**shape, ws=P(at + inside)) == w4.ERR_SHAPE
         for beside in (size, -need):
             assert gemm(**shape, ws=P(at + beside)) == w4.OK
+
+
+def lay_out(**kw):
+    """The call itself: of buffers that overlap it is refused before any launch."""
+    a = dict(codes=P(), scales=P(1 << 31), E=2, N=40, K=264, q=P(1 << 33), s=P(1 << 34))
+    a.update(kw)
+    return mx._mx().w4a16_mx_weight(*a.values(), None)
+
+
+def test_the_layout_in_place_is_refused():
+    codes, scales = 2 * 40 * 256, 2 * 40 * 16
+    q, s = mx.weight_size(2, 40, 264)
+    for at, size in ((0, codes), (1 << 31, scales)):
+        for inside in (0, size - 16):
+            assert lay_out(q=P(at + inside)) == w4.ERR_SHAPE
+            assert lay_out(s=P(at + inside)) == w4.ERR_SHAPE
+        assert lay_out(q=P(at + 16 - q)) == w4.ERR_SHAPE
+        assert lay_out(s=P(at + 16 - s)) == w4.ERR_SHAPE
+    assert lay_out(s=P((1 << 33) + q - 16)) == w4.ERR_SHAPE
+    assert lay_out(q=P((1 << 34) + s - 16)) == w4.ERR_SHAPE

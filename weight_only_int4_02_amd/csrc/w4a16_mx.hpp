@@ -38,6 +38,10 @@ struct MxPlan {
 };
 MxPlan plan_mx(int64_t R, int64_t E, int64_t N, int64_t K, bool fp4, bool grouped);
 
+// Whether a result of w4a16_mx_weight overlaps the other or an input.
+bool weight_overlaps(const void *codes, const void *scales, int64_t E, int64_t N, int64_t K,
+                     const void *q_dev, const void *s_dev);
+
 int launch_mx_quantize(const void *X, int dtype, int64_t M, int64_t K, uint8_t *codes,
                        uint8_t *scales, void *stream);
 int launch_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K,

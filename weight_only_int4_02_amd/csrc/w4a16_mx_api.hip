@@ -67,8 +67,10 @@ int32_t w4a16_mx_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t
 
 int32_t w4a16_mx_weight(const uint8_t *codes, const uint8_t *scales, int64_t E, int64_t N,
                         int64_t K, void *q_dev, void *s_dev, void *stream) {
-    return enqueue("w4a16_mx_weight",
-                   w4a16_mx_check_weight_args(codes, scales, E, N, K, q_dev, s_dev),
+    int32_t st = w4a16_mx_check_weight_args(codes, scales, E, N, K, q_dev, s_dev);
+    if (!st && weight_overlaps(codes, scales, E, N, K, q_dev, s_dev))
+        st = W4A16_ERR_SHAPE;
+    return enqueue("w4a16_mx_weight", st,
                    [&] { return launch_mx_weight(codes, scales, E, N, K, q_dev, s_dev, stream); });
 }
 

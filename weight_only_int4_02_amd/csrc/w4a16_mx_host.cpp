@@ -72,6 +72,14 @@ int32_t check_product(const void *X, const uint8_t *x_scales, int32_t x_dtype, i
 
 }  // namespace
 
+bool weight_overlaps(const void *codes, const void *scales, int64_t E, int64_t N, int64_t K,
+                     const void *q_dev, const void *s_dev) {
+    const int64_t rows = E * N * kslabs(K);
+    return overlaps_weight(codes, rows * 256, q_dev, s_dev, E, N, K) ||
+           overlaps_weight(scales, rows * 16, q_dev, s_dev, E, N, K) ||
+           overlap(q_dev, weight_q_bytes(E, N, K), s_dev, weight_s_bytes(E, N, K));
+}
+
 // The large kernel's output tiles: workgroups that share a compute unit, whether K
 // may be split over workgroups, and microseconds: of a stage (64 columns of
 // 16-bit activations, 256 of MXFP4) what a workgroup needs at least (`alone`: the
