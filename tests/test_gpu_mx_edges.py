@@ -65,3 +65,18 @@ def test_grouped_one_row_for_many(T, K, R, N, quantized):
         want, bound = ref.product(xv, wv[e], torch.bfloat16)
         index = rows[mine].long()
         compare(y[mine], want[index], bound[index])
+
+
+# ---- a checkpoint's codes and scales ----------------------------------------------
+@pytest.mark.parametrize("rows", [(1,), (3,), (2, 5), ()])
+@pytest.mark.parametrize("K", [8, 40, 488, 504, 512, 1024])
+def test_tensor_keeps_nothing_of_what_it_is_given(K, rows):
+    """A loader's staging buffers may be filled again right after the call, whatever
+    K is."""
+    code = torch.randint(0, 16, (*rows, K), generator=gen(K), dtype=torch.uint8)
+    scale = torch.randint(100, 150, (*rows, -(-K // 32)), generator=gen(K + 1), dtype=torch.uint8)
+    codes, scales = ref.pack(code).cuda(), scale.cuda()
+    t = mx.tensor(codes, scales, K)
+    codes.fill_(0x77)
+    scales.fill_(255)
+    assert torch.equal(mx.dequantize(t, torch.float32).cpu().double(), ref.values(code, scale))

@@ -172,8 +172,8 @@ def dequantize(t: MXTensor, dtype: Optional[torch.dtype] = None) -> torch.Tensor
 def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
            dtype: torch.dtype = torch.bfloat16) -> MXTensor:
     """codes uint8 [.., K/2] and scales uint8 [.., ceil(K/32)], as checkpoints hold
-    them, on the device -> MXTensor (padded to whole slabs of 512 columns).  K:
-    twice the codes' last dimension if None."""
+    them, on the device -> MXTensor (a copy, padded to whole slabs of 512 columns).
+    K: twice the codes' last dimension if None."""
     device = _device_of(codes, "codes")
     if codes.dim() < 1:
         raise ValueError("codes must have at least one dimension")
@@ -191,8 +191,10 @@ def tensor(codes: torch.Tensor, scales: torch.Tensor, K: Optional[int] = None,
         codes = torch.nn.functional.pad(codes, (0, 256 * KG - codes.shape[-1]))
     if scales.shape[-1] != 16 * KG:
         scales = torch.nn.functional.pad(scales, (0, 16 * KG - scales.shape[-1]), value=127)
-    codes = codes.unflatten(-1, (4 * KG, 64)).movedim(-2, 0).contiguous()
-    scales = scales.unflatten(-1, (KG, 16)).movedim(-2, 0).contiguous()
+    # (a copy in any case: where no padding is needed and the order is the same, a
+    # view would change with the caller's buffers)
+    codes = codes.unflatten(-1, (4 * KG, 64)).movedim(-2, 0).clone(memory_format=torch.contiguous_format)
+    scales = scales.unflatten(-1, (KG, 16)).movedim(-2, 0).clone(memory_format=torch.contiguous_format)
     return MXTensor(codes, scales, K, dtype)
 
 
