@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from oracle import mx as ref
-from test_gpu_mx import compare, device_weight, gen, operands, random_weight
+from test_gpu_mx import DT, compare, device_weight, gen, operands, random_weight
 from weight_only_int4_02_amd import mx
 
 pytestmark = [pytest.mark.gpu,
@@ -80,3 +80,22 @@ def test_tensor_keeps_nothing_of_what_it_is_given(K, rows):
     codes.fill_(0x77)
     scales.fill_(255)
     assert torch.equal(mx.dequantize(t, torch.float32).cpu().double(), ref.values(code, scale))
+
+
+# ---- values and scales at the ends of their ranges ---------------------------------
+@pytest.mark.parametrize("M", [4, 100])
+@pytest.mark.parametrize("dt,quantized,low,high,x_exponent", [
+    ("bf16", False, 0, 4, 120), ("bf16", False, 245, 250, -130), ("bf16", False, 118, 126, -128),
+    ("bf16", False, 40, 60, -60), ("f16", False, 135, 140, -20), ("f16", False, 118, 126, -15),
+    ("f16", False, 104, 110, 10), ("bf16", True, 40, 60, -60), ("bf16", True, 250, 254, -110),
+    ("bf16", True, 0, 4, 120), ("bf16", True, 180, 186, 60)])
+def test_gemm_subnormal_values(dt, quantized, low, high, x_exponent, M):
+    """Subnormal weights, activations and results count in full, and scales of both
+    ends meet.  (Sums in 32 bits below 2^-126 are off by 2^-149 each besides: 2 K of
+    them are far below half a step of the results, 2^-134 in bf16.)"""
+    N, K = 40, 200
+    x = (torch.randn((M, K), generator=gen(1)).double() * 2.0 ** x_exponent).to(DT[dt])
+    code, scale = random_weight((N, K), 2, low, high)
+    X, xv, wv = operands(x, code, scale, quantized)
+    want, bound = ref.product(xv, wv, DT[dt])
+    compare(mx.gemm(X, device_weight(code, scale)), want, bound + 2 * K * 2.0 ** -149)

@@ -1,0 +1,147 @@
+"""Every form of the microscaled 4-bit products in each type that it has, along K
+of more than two slabs of scales (and more stages than a ring holds), on operands
+whose sums 32 bits hold exactly.
+
+Operands are MXFP4 values with two scales each: a product of two is a whole
+number of units of 2^-12 (1/2 and 1/2 with the scales 2^-1 and 2^-9), and the
+magnitudes of a result's products sum to less than 2^24 units.  So every partial
+sum, in whatever order, is a number of 32 bits, and the result is the exact sum
+rounded once: it has to be equal.  Most signs are alike, so that sums need more
+bits than 16-bit types have: one kept in 16 bits on the way, a product lost or one
+from a neighbouring column shows."""
+import pytest
+import torch
+
+from oracle import mx as ref
+from test_gpu_mx import DT, FORMS16, GROUPED16, LAST_ROWS, compare_all, device_weight, gen, random_weight, weight_values
+from weight_only_int4_02_amd import mx
+
+pytestmark = [pytest.mark.gpu,
+              pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU")]
+
+# (rows, N, K[, experts]): a shape of long K for each form that the plans choose; of those whose
+# workgroups stay, with more tiles than compute units
+DEEP16 = [(1618, 4878, 1080), (5584, 74, 1584), (4161, 1411, 1040), (5807, 138, 3424), (2330, 12362, 1040),
+          (5442, 85, 1080), (70, 67, 1176), (66, 16614, 1192), (797, 140, 4144), (1, 34, 1064), (1, 33, 8552),
+          (1, 4268, 1064), (1, 8635, 1048), (17, 34, 1056), (17, 4509, 1192), (20, 8525, 1064), (33, 33, 1064),
+          (33, 4102, 1312), (37, 8785, 1048), (53, 34, 1104), (49, 4243, 1144), (50, 9601, 1104), (65, 18, 4440),
+          (61, 64, 11008)]
+DEEP4 = [(6972, 1026, 1136), (74, 16635, 8840), (792, 16588, 1056), (4816, 4513, 1096), (65, 68, 1200), (73, 67, 1328),
+         (1, 33, 1056), (2, 33, 8096), (1, 4163, 1120), (1, 8820, 1048), (20, 33, 1088), (17, 33, 8560),
+         (18, 4489, 1072), (17, 8678, 1168), (35, 35, 1072), (33, 4145, 1208), (34, 8434, 1096), (50, 34, 1112),
+         (50, 4377, 1176), (50, 9222, 1072), (61, 64, 11008)]
+DEEP_GROUPED16 = [(10697, 86, 1072, 188), (15645, 131, 1096, 108), (26621, 844, 1128, 4), (68, 69, 1376, 2),
+                  (3668, 146, 1160, 132), (176, 1589, 1056, 168), (185, 337, 1096, 180), (8, 42, 1072, 2),
+                  (20, 46, 1056, 2)]
+DEEP_GROUPED4 = [(9470, 69, 1336, 250), (16929, 667, 1120, 49), (4436, 5002, 1056, 5), (15, 81, 1104, 2),
+                 (46, 6715, 1088, 41), (106, 658, 1056, 96), (9, 35, 1096, 2)]
+TYPES16 = ["f16", "bf16"]       # of 16-bit activations; of quantized ones the results' only
+UNIT = 2.0 ** -12
+
+
+def codes_of(shape, seed, low):
+    """Codes of which one in eight is negative, and scale bytes low or low + 1, on the
+    device."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    code = torch.randint(0, 8, shape, generator=g, dtype=torch.uint8, device="cuda")
+    code += 8 * (torch.randint(0, 8, shape, generator=g, dtype=torch.uint8, device="cuda") == 0)
+    scale = torch.randint(low, low + 2, (*shape[:-1], -(-shape[-1] // 32)), generator=g, dtype=torch.uint8, device="cuda")
+    return code, scale
+
+
+def values_of(code, scale):
+    v = ref.SIZES.cuda()[(code & 7).long()] * torch.where(code >= 8, -1.0, 1.0).double()
+    return v * torch.exp2(scale.double() - 127).repeat_interleave(32, -1)[..., :code.shape[-1]]
+
+
+def activations(T, K, dt, quantized, seed):
+    """(what the product is given, its values)"""
+    code, scale = codes_of((T, K), seed, 126)
+    v = values_of(code, scale)
+    return mx.tensor(ref.pack(code), scale, K, dtype=DT[dt]) if quantized else v.to(DT[dt]), v
+
+
+def weight_of(shape, seed):
+    code, scale = codes_of(shape, seed, 118)
+    return mx.weight(mx.tensor(ref.pack(code), scale, shape[-1])), code, scale
+
+
+def check_equal(y, X, code, scale):
+    W = values_of(code, scale)
+    assert float((X.abs() @ W.abs().T).max()) < 2 ** 24 * UNIT
+    want = X @ W.T
+    assert float(want.abs().max()) > 2 ** 12 * UNIT
+    assert torch.equal(y, want.to(y.dtype))
+
+
+@pytest.mark.parametrize("dt", TYPES16)
+@pytest.mark.parametrize("quantized,shape", [(False, s) for s in DEEP16] + [(True, s) for s in DEEP4])
+def test_gemm_long_k(shape, quantized, dt):
+    M, N, K = shape
+    X, xv = activations(M, K, dt, quantized, M + K)
+    w, code, scale = weight_of((N, K), N)
+    y = mx.gemm(X, w)
+    assert y.dtype == DT[dt]
+    check_equal(y, xv, code, scale)
+
+
+def check_grouped(counts, N, K, dt, quantized, gather, seed):
+    E, R = len(counts), sum(counts)
+    T = R // 2 + 1 if gather else R
+    X, xv = activations(T, K, dt, quantized, seed)
+    w, code, scale = weight_of((E, N, K), seed + 1)
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    rows = torch.randint(0, T, (R,), generator=gen(seed + 2), dtype=torch.int32).cuda() if gather else None
+    y = mx.grouped_gemm(X, w, offsets.cuda(), rows=rows)
+    for e in range(E):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.stop > mine.start:
+            check_equal(y[mine], xv[rows[mine].long()] if gather else xv[mine], code[e], scale[e])
+
+
+@pytest.mark.parametrize("dt", TYPES16)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("quantized,shape", [(False, s) for s in DEEP_GROUPED16] + [(True, s) for s in DEEP_GROUPED4])
+def test_grouped_long_k(shape, quantized, gather, dt):
+    R, N, K, E = shape
+    counts = torch.bincount(torch.randint(0, E, (R,), generator=gen(R)), minlength=E).tolist()
+    check_grouped(counts, N, K, dt, quantized, gather, N)
+
+
+LAST_TILES = [(False, 20, 1032, "64x128"), (False, 258, 1032, "64x256"), (False, 517, 1032, "128x128"),
+              (False, 661, 1032, "128x256"), (False, 1820, 1032, "256x256"), (True, 20, 1032, "64x128"),
+              (True, 258, 1032, "128x128"), (True, 661, 1032, "128x256"), (True, 1332, 1032, "256x256")]
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("quantized,N,K,tile", LAST_TILES)
+def test_grouped_last_tiles_long_k(quantized, N, K, tile, gather):
+    assert mx.kernel(sum(LAST_ROWS), N, K, quantized, len(LAST_ROWS))[:2] == ("large", tile)
+    for order in (LAST_ROWS, LAST_ROWS[::-1]):
+        check_grouped(order, N, K, "bf16", quantized, gather, N)
+
+
+# ---- the other type at the shapes of the forms ------------------------------------
+@pytest.mark.parametrize("shape", FORMS16)
+def test_gemm_forms_fp16(shape):
+    M, N, K = shape
+    x = torch.randn((M, K), generator=gen(M)).half().cuda()
+    code, scale = random_weight((N, K), N)
+    compare_all(mx.gemm(x, device_weight(code, scale)), x.double(), weight_values(code, scale, x.dtype, False))
+
+
+@pytest.mark.parametrize("shape", GROUPED16)
+def test_grouped_forms_bf16(shape):
+    R, N, K, E = shape
+    T = R // 2 + 1
+    x = torch.randn((T, K), generator=gen(R)).to(torch.bfloat16).cuda()
+    code, scale = random_weight((E, N, K), N)
+    ids = torch.randint(0, E, (R,), generator=gen(R + 1)).sort().values
+    offsets = torch.searchsorted(ids, torch.arange(E + 1)).to(torch.int32)
+    rows = torch.randint(0, T, (R,), generator=gen(R + 2), dtype=torch.int32).cuda()
+    y = mx.grouped_gemm(x, device_weight(code, scale), offsets.cuda(), rows=rows)
+    wv = weight_values(code, scale, x.dtype, False)
+    for e in range(E):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.stop > mine.start:
+            compare_all(y[mine], x.double()[rows[mine].long()], wv[e])

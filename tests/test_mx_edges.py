@@ -69,3 +69,31 @@ def test_the_layout_in_place_is_refused():
         assert lay_out(s=P(at + 16 - s)) == w4.ERR_SHAPE
     assert lay_out(s=P((1 << 33) + q - 16)) == w4.ERR_SHAPE
     assert lay_out(q=P((1 << 34) + s - 16)) == w4.ERR_SHAPE
+
+
+# ---- the forms along a long K ------------------------------------------------------
+def test_the_gpu_tests_have_a_shape_of_long_k_for_every_form():
+    """Every form that some call with K of more than two slabs takes is among those
+    of the shapes that test_gpu_mx_forms.py checks, in every type."""
+    import random
+
+    import test_gpu_mx_forms as t
+    from test_mx_abi import form
+    rng = random.Random(1)
+
+    def spread(lo, hi):
+        return int(round(lo * (hi / lo) ** rng.random()))
+
+    have = {q: ({form(*s, q) for s in plain}, {form(*s[:3], q, s[3]) for s in grouped})
+            for q, plain, grouped in ((False, t.DEEP16, t.DEEP_GROUPED16), (True, t.DEEP4, t.DEEP_GROUPED4))}
+    for shapes in (t.DEEP16, t.DEEP4, t.DEEP_GROUPED16, t.DEEP_GROUPED4):
+        assert all(s[2] > 1024 and (s[2] % 512 or s[2] > 2048) for s in shapes)
+    assert t.TYPES16 == ["f16", "bf16"]
+    for _ in range(6000):
+        q = rng.random() < 0.5
+        R, N, K = spread(1, 8192), spread(1, 32000), 8 * spread(130, 1400)
+        assert form(R, N, K, q) in have[q][0], (R, N, K, q)
+        R, N, K, E = spread(1, 30000), spread(1, 8000), 8 * spread(130, 800), spread(1, 256)
+        assert form(R, N, K, q, E) in have[q][1], (R, N, K, E, q)
+    for q, N, K, tile in t.LAST_TILES:
+        assert mx.kernel(sum(t.LAST_ROWS), N, K, q, len(t.LAST_ROWS))[:2] == ("large", tile)
