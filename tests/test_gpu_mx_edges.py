@@ -99,3 +99,23 @@ def test_gemm_subnormal_values(dt, quantized, low, high, x_exponent, M):
     X, xv, wv = operands(x, code, scale, quantized)
     want, bound = ref.product(xv, wv, DT[dt])
     compare(mx.gemm(X, device_weight(code, scale)), want, bound + 2 * K * 2.0 ** -149)
+
+
+# ---- rows of zeros beside weights that are not finite -------------------------------
+@pytest.mark.parametrize("quantized", [False, True])
+@pytest.mark.parametrize("R", [9, 400])
+def test_grouped_index_outside_beside_nan(R, quantized):
+    """An index outside X counts as a row of zeros: results are 0, and NaN where a
+    weight is."""
+    T, N, K = 4, 40, 136
+    x = torch.randn((T, K), generator=gen(6)).to(torch.bfloat16)
+    code, scale = random_weight((1, N, K), 7)
+    scale[0, 17, 2] = 255
+    X, xv, wv = operands(x, code, scale, quantized)
+    rows = torch.randint(0, T, (R,), generator=gen(8), dtype=torch.int32)
+    rows[::3] = T
+    offsets = torch.tensor([0, R], dtype=torch.int32)
+    y = mx.grouped_gemm(X, device_weight(code, scale), offsets.cuda(), rows=rows.cuda())
+    want, bound, _ = ref.grouped(xv, wv, offsets, rows, torch.bfloat16)
+    compare(y, want, bound)
+    assert bool(y[::3, 17].isnan().all()) and int((y[::3] == 0).sum()) == (N - 1) * len(rows[::3])

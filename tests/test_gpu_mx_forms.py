@@ -70,7 +70,6 @@ def check_equal(y, X, code, scale):
     W = values_of(code, scale)
     assert float((X.abs() @ W.abs().T).max()) < 2 ** 24 * UNIT
     want = X @ W.T
-    assert float(want.abs().max()) > 2 ** 12 * UNIT
     assert torch.equal(y, want.to(y.dtype))
 
 
@@ -83,6 +82,7 @@ def test_gemm_long_k(shape, quantized, dt):
     y = mx.gemm(X, w)
     assert y.dtype == DT[dt]
     check_equal(y, xv, code, scale)
+    assert float(y.abs().max()) > 2 ** 12 * UNIT
 
 
 def check_grouped(counts, N, K, dt, quantized, gather, seed):
@@ -145,3 +145,34 @@ def test_grouped_forms_bf16(shape):
         mine = slice(int(offsets[e]), int(offsets[e + 1]))
         if mine.stop > mine.start:
             compare_all(y[mine], x.double()[rows[mine].long()], wv[e])
+
+
+# ---- many experts, and rows of none, for the tiles that stay and those that do not ----
+@pytest.mark.parametrize("E", [1000, 1024])
+@pytest.mark.parametrize("quantized,R,N,tile", [
+    (False, 20000, 150, "64x256"), (False, 150000, 150, "128x256"), (False, 350000, 260, "256x256"),
+    (True, 8000, 260, "64x128"), (True, 8000, 150, "128x256"), (True, 150000, 260, "256x256")])
+def test_grouped_many_experts_large_tiles(quantized, R, N, tile, E):
+    K = 584
+    assert mx.kernel(R, N, K, quantized, E)[:2] == ("large", tile)
+    g = gen(E)
+    like = torch.rand(E, generator=g) * (torch.rand(E, generator=g) < 0.6)     # four in ten have no rows
+    counts = torch.bincount(torch.multinomial(like, R, replacement=True, generator=g), minlength=E).tolist()
+    check_grouped(counts, N, K, "bf16", quantized, True, E)
+
+
+@pytest.mark.parametrize("quantized,N,K,tile", LAST_TILES)
+def test_grouped_rows_of_no_expert_stay_for_every_tile(quantized, N, K, tile):
+    counts, first = [n if n != 449 else 149 for n in LAST_ROWS], 5
+    E, R, used = len(counts), sum(LAST_ROWS), sum(counts)      # (295 rows behind the last expert's)
+    assert mx.kernel(R, N, K, quantized, E)[:2] == ("large", tile)
+    X, xv = activations(R, K, "f16", quantized, N)
+    w, code, scale = weight_of((E, N, K), N + 1)
+    offsets = torch.tensor([0] + counts).cumsum(0).to(torch.int32) + first
+    out = torch.full((R, N), 77.0, dtype=torch.float16, device="cuda")
+    assert mx.grouped_gemm(X, w, offsets.cuda(), out=out) is out
+    assert bool((out[:first] == 77.0).all()) and bool((out[first + used:] == 77.0).all())
+    for e in range(E):
+        mine = slice(int(offsets[e]), int(offsets[e + 1]))
+        if mine.stop > mine.start:
+            check_equal(out[mine], xv[mine], code[e], scale[e])
