@@ -73,7 +73,8 @@ int32_t w4a16_mx_check_weight_args(const uint8_t *codes, const uint8_t *scales, 
 
 /* Y [M][N] = X [M][K] . W^T, with fp32 sums, rounded once.
  *   x_scales NULL: X is 16-bit (x_dtype), and a weight enters as its value
- *     rounded to that type (exact in bf16; in fp16 for scales of 2^-23 .. 2^13);
+ *     rounded to that type (exact in bf16 but for magnitudes past its largest; in
+ *     fp16 for scales of 2^-23 .. 2^13, infinite for larger values than it has);
  *   else X and x_scales are MXFP4 rows, multiplied by the matrix cores' scaled
  *     instruction.
  * y_dtype: fp16 or bf16; of a 16-bit X, its own.
@@ -100,8 +101,8 @@ int32_t w4a16_mx_check_gemm_args(const void *X, const uint8_t *x_scales, int32_t
  * with rows NULL: X[i].  X [T][K] as in w4a16_mx_gemm, rows int32 [R],
  * offsets int32 [E + 1], Y [R][N]; with rows NULL, T = R.
  * offsets rise from 0 or more to R or less.  Rows of Y before the first and
- * from the last offset on stay as they are.  An index outside 0 .. T - 1 gives
- * a row of zeros.  Offsets live on the device and are not checked: values
+ * from the last offset on stay as they are.  An index outside 0 .. T - 1 counts
+ * as a row of zeros (NaN comes of it where the weight is not finite).  Offsets live on the device and are not checked: values
  * outside 0 .. R are taken as 0 or R, and where they fall, which rows are
  * written, and with what, is not defined (nothing outside Y is).
  * Limits: those of w4a16_mx_gemm, R < 2^31.

@@ -47,8 +47,9 @@ __device__ __forceinline__ uint32_t dpp(uint32_t v) {
 
 // A workgroup takes four rows of a slab of 512 columns: a wave 128 columns of
 // each, a lane eight of one row, so that reads are runs of 1 KiB (16 bits) and the
-// codes of a wave one run of 256 bytes (22016 x 4096 in bf16 48 us, 4.8 TB/s, its
-// inverse 33, 6.9; with four tiles of one row a wave 88 together).  Four neighbouring
+// codes of a wave one run of 256 bytes (22016 x 4096 in bf16 47 us, 4.8 TB/s, its
+// inverse 33, 6.9 with codes that the caches still hold; with four tiles of one row a
+// wave 88 together).  Four neighbouring
 // lanes share a block.  The largest magnitude is found on the bits (whose order is
 // that of the magnitudes, NaN above infinity above numbers): its exponent field
 // less two is the scale byte.

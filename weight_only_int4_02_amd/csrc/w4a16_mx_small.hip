@@ -11,7 +11,7 @@
 // by buffer-to-LDS DMA, whole runs of a row at a time, and reads the operands from
 // there (loaded straight into operand registers, a lane's 16 bytes lie a row away
 // from its neighbours' and are a request of their own: 32 x 12288 x 4096 in bf16
-// took 16.4 us so, of which 5.8 were those loads; now 11.8).  A row's blocks of
+// took 16.4 us so, of which 5.8 were those loads; now 10.2).  A row's blocks of
 // 16 bytes stand in an order that gives the lanes of a read (one block of 16 rows)
 // different banks.  No wave waits for another before the sums.
 //
@@ -22,9 +22,12 @@
 //
 // All loads are untracked (see load_b128_so): a stage is waited for by counting.
 //
-// Bound by the weights' bytes, and at these sizes by latency: 4096 x 4096, one row,
-// 5.3 us (1.7 TB/s), 12288 x 4096, 32 rows, 10.1 (2.7), two experts of 22016 x 4096,
-// one row each, 20.3 (4.7), 64 of 2048 x 1408, 1.5 rows each, 15.4 (5.1).
+// Bound by the weights' bytes where there are many: two experts of 22016 x 4096, one
+// row each, 20.5 us (4.7 TB/s), 64 of 2048 x 1408, 1.5 rows each, 15.5 (5.0).  Below
+// that launch and latency count: 4096 x 4096, one row, 5.3 (1.7), 12288 x 4096, 32 rows,
+// 10.2 (2.6), whose workgroups read 67 MB of activations out of L2 beside 27 of weights.
+// LDS is busy 0.05 .. 0.08 of the time, without bank conflicts, the matrix cores
+// 0.05 .. 0.14.
 #include <hip/hip_runtime.h>
 
 #include "w4a16_mx_device.hpp"

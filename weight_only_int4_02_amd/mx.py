@@ -28,7 +28,6 @@ from . import _raise, lib
 from .moe import check, stream_of
 
 BLOCK = 32
-MAX_EXPERTS = 1024
 
 # Symbols of include/w4a16_mx.h.
 EXPORTS = ("w4a16_mx_quantize", "w4a16_mx_check_quantize_args", "w4a16_mx_dequantize",
